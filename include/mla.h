@@ -22,7 +22,9 @@
  * mla_decode_attend + mla_decode_finish; mla_decode_static without a
  * workspace), with mla_decode_cudacore + mla_splitkv_combine as an
  * independent CUDA-core path of the same decode.  Long prefill chunks use
- * mla_prefill_naive (the naive form) after mla_append_cache.
+ * mla_prefill_naive (the naive form) after mla_append_cache.  With the cache
+ * held in 8 bits: mla_append_cache8 and mla_decode8; mla_read_cache8 brings
+ * sequences back into a bf16 cache.
  *
  * Fixed sizes: d_c = 512, d_h^R = 64, d_h = 128 (cached row D = 576).
  * Runtime sizes: B sequences, H heads (1..128), n_q new query tokens per
@@ -87,6 +89,7 @@ typedef void* mla_stream; /* cudaStream_t */
 
 #define MLA_BLOCK_TOKENS 128
 #define MLA_BLOCK_BYTES 147456
+#define MLA_BLOCK8_BYTES 74240 /* a block of the 8-bit cache (mla_append_cache8) */
 
 typedef enum {
     MLA_OK = 0,
@@ -207,6 +210,78 @@ mla_status mla_append_cache(void* cache, int64_t cap_blocks, const int32_t* bloc
                             int num_seqs, int max_blocks, const int32_t* seq_idx, const int32_t* pos,
                             const void* c_kv, const void* k_rope, const float* rope_table,
                             int64_t rope_len, int T, int32_t* dev_status, mla_stream stream);
+
+/*
+ * mla_append_cache8 -- write T new tokens into a latent cache held in 8 bits.
+ * (The cache is what bounds MLA decode; the pages keep it in 16 bits.  The
+ *  8-bit form is this library's: half the bytes to read a step, twice the
+ *  tokens in the same memory.)
+ *   cache8       pool of cap_blocks blocks of MLA_BLOCK8_BYTES
+ *   other arguments and their checks: as mla_append_cache
+ * The row x = [c^KV (512) | R_pos k^R (64)] in bf16 is exactly the one that
+ * mla_append_cache stores.  Its 8-bit form is one fp32 scale and 576 codes:
+ *   s      = 2^k, the least power of two >= 2^-40 with max |x_i| <= 448 s over
+ *            the finite x_i; s = 1 if none of them is nonzero
+ *   code_i = e4m3(x_i / s), round to nearest, ties to even; NaN and
+ *            infinities are stored as NaN
+ * and code_i * s stands for x_i.  The scale is a power of two so that it adds
+ * no rounding of its own; it covers one token, so that a step's new token
+ * never changes what is already stored.  Error: at most 2^-4 |x_i| for
+ * |x_i| >= 2^-6 s, at most 2^-10 s below.
+ * Layout of a block (128 tokens): column c of row r at byte
+ *   c <  512: (c / 128) * 16384 + r * 128 + (((c % 128) / 16) ^ (r % 8)) * 16 + c % 16
+ *   c >= 512: 65536 + r * 64 + (((c - 512) / 16) ^ (r / 2 % 4)) * 16 + c % 16
+ * (the 128-byte and 64-byte swizzles of the tensor-core operands), the scale
+ * of row r at byte 73728 + 4 r.
+ */
+mla_status mla_append_cache8(void* cache8, int64_t cap_blocks, const int32_t* block_table,
+                             int num_seqs, int max_blocks, const int32_t* seq_idx, const int32_t* pos,
+                             const void* c_kv, const void* k_rope, const float* rope_table,
+                             int64_t rope_len, int T, int32_t* dev_status, mla_stream stream);
+
+/*
+ * mla_read_cache8 -- bring sequences of an 8-bit cache back into a bf16 cache.
+ * For every sequence b and token t < kv_len[b]: row t of sequence b in
+ * `cache` (through block_table) = bf16(code_i * s) of the same token in
+ * `cache8` (through block_table8), so that calls that read a bf16 cache, such
+ * as mla_prefill_naive for a chunk behind an 8-bit prefix, can use it.  Rows
+ * from kv_len[b] on, and blocks of no sequence, are left as they were.
+ *   cache8  pool of cap_blocks8 blocks of MLA_BLOCK8_BYTES;  block_table8
+ *           int32 [B, max_blocks8]
+ *   cache   pool of cap_blocks blocks of MLA_BLOCK_BYTES;  block_table int32
+ *           [B, max_blocks]; no block of it may be named twice among the
+ *           blocks that are written
+ *   kv_len  int32 [B]: tokens to bring back (0: none)
+ * code * s is exact in bf16 but at the ends of its range (|y| < 2^-126, and a
+ * row whose largest value rounds up to 2^128, which reads back as infinity).
+ * A sequence with kv_len[b] < 0 sets MLA_DEVERR_KV_LEN, one that does not fit
+ * either of its table rows sets MLA_DEVERR_ROW_RANGE; neither is copied.  A
+ * block whose entry lies outside its pool sets MLA_DEVERR_ROW_RANGE and is
+ * skipped.  Errors: MLA_ERR_INVALID_ARG for null or misaligned pointers and
+ * negative sizes (before any launch).  B = 0 launches nothing.
+ */
+mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_t* block_table8,
+                           int max_blocks8, const int32_t* kv_len, int B, void* cache,
+                           int64_t cap_blocks, const int32_t* block_table, int max_blocks,
+                           int32_t* dev_status, mla_stream stream);
+
+/*
+ * mla_decode8_workspace_bytes / mla_decode8 -- mla_decode over an 8-bit cache:
+ * the same step, with c_t = s_t code_t (512 latent and 64 RoPE columns) in the
+ * place of the bf16 rows.  Arguments, shapes, results and errors are those of
+ * mla_decode, but for
+ *   cache8     pool of cap_blocks blocks of MLA_BLOCK8_BYTES, written by
+ *              mla_append_cache8 (bytes of no token are never used)
+ *   workspace  of at least mla_decode8_workspace_bytes() bytes
+ * The query stays bf16 and scores are formed from it and the codes without a
+ * further rounding of either; sums, softmax and scales are fp32.
+ */
+size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits);
+mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks,
+                       const int32_t* block_table, int max_blocks, const int32_t* kv_len,
+                       const void* W_UV, int B, int n_q, int H, float scale, int num_splits,
+                       void* workspace, size_t ws_bytes, void* out, float* lse_out,
+                       int32_t* dev_status, mla_stream stream);
 
 /*
  * mla_decode_workspace_bytes -- device workspace mla_decode needs for these

@@ -10,6 +10,7 @@ loudly if the shared library has not been built
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -19,6 +20,7 @@ D_C, D_R, D_H = 512, 64, 128
 D_ROW = D_C + D_R
 BLOCK_TOKENS = 128      # tokens per cache block
 BLOCK_BYTES = 147456    # 9 chunks x [128 rows x 128 bytes]
+BLOCK8_BYTES = 74240    # 8-bit cache: 576 e4m3 codes and one fp32 scale a token
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmla_b200.so")
 if not os.path.exists(_LIB_PATH):
@@ -37,6 +39,10 @@ _SIGS = {
     "mla_query_up": ([_p, _p, _p, _i32, _i32, _i32, _p, _p, _p, _p], _i32),
     "mla_query_absorb": ([_p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _p, _p], _i32),
     "mla_append_cache": ([_p, _i64, _p, _i32, _i32, _p, _p, _p, _p, _p, _i64, _i32, _p, _p], _i32),
+    "mla_append_cache8": ([_p, _i64, _p, _i32, _i32, _p, _p, _p, _p, _p, _i64, _i32, _p, _p], _i32),
+    "mla_read_cache8": ([_p, _i64, _p, _i32, _p, _i32, _p, _i64, _p, _i32, _p, _p], _i32),
+    "mla_decode8_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
+    "mla_decode8": ([_p, _p, _i64, _p, _i32, _p, _p, _i32, _i32, _i32, _f32, _i32, _p, _sz, _p, _p, _p, _p], _i32),
     "mla_decode_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
     "mla_decode": ([_p, _p, _i64, _p, _i32, _p, _p, _i32, _i32, _i32, _f32, _i32, _p, _sz, _p, _p, _p, _p], _i32),
     "mla_decode_attend": ([_p, _p, _i64, _p, _i32, _p, _i32, _i32, _i32, _f32, _i32, _p, _sz, _p, _p], _i32),
@@ -88,6 +94,23 @@ def _ptr(t: torch.Tensor | None, dtype=None, shape=None, name="tensor"):
 def _stream(stream) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+def _on(stream, **tensors):
+    """Context of a call whose tensors are all on one device: that device is the current one, and ``stream`` (a
+    torch stream; None: the device's current one) too, so that what the call allocates belongs to that stream."""
+    devs = {t.device for t in tensors.values() if t is not None and t.is_cuda}
+    if len(devs) > 1 or (stream is not None and devs and stream.device not in devs):
+        raise MLAError("tensors and stream must be on one device")
+    if not devs:
+        return contextlib.nullcontext()  # no CUDA tensor: the checks of the arguments say which
+    return torch.cuda.device(devs.pop()) if stream is None else torch.cuda.stream(stream)
+
+
+def _rope_ptr(rope_tab):
+    if rope_tab.dim() != 2 or rope_tab.shape[1] != D_R:
+        raise MLAError(f"rope_table must be float32 [rope_len, {D_R}]")
+    return _ptr(rope_tab, torch.float32, None, "rope_table")
 
 
 def rope_table(rope_len: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -189,6 +212,71 @@ def append_cache(cache, block_table, seq_idx, pos, c_kv, k_rope, rope_tab, dev_s
         _ptr(c_kv, torch.bfloat16, (T, D_C), "c_kv"), _ptr(k_rope, torch.bfloat16, (T, D_R), "k_rope"),
         _ptr(rope_tab, torch.float32, None, "rope_table"), rope_tab.shape[0], T,
         _ptr(dev_status, torch.int32, None, "dev_status"), _stream(stream)))
+
+
+def new_cache8(cap_blocks: int, device="cuda") -> torch.Tensor:
+    """An empty pool of 8-bit cache blocks: uint8 [cap_blocks, BLOCK8_BYTES] (layout in include/mla.h)."""
+    return torch.empty((cap_blocks, BLOCK8_BYTES), dtype=torch.uint8, device=device)
+
+
+def _cache8_ptr(cache8):
+    if cache8.dim() != 2 or cache8.shape[1] != BLOCK8_BYTES:
+        raise MLAError(f"cache8 must be uint8 [cap_blocks, {BLOCK8_BYTES}]")
+    return _ptr(cache8, torch.uint8, None, "cache8")
+
+
+def append_cache8(cache8, block_table, seq_idx, pos, c_kv, k_rope, rope_tab, dev_status=None, stream=None):
+    """Quantise the rows [c_kv [T,512] | R_pos k_rope [T,64]] to 576 e4m3 codes and a power-of-two scale each and
+    write them at token pos of sequence seq_idx of an 8-bit cache."""
+    T = c_kv.shape[0]
+    tp, mb = _table(block_table)
+    with _on(stream, cache8=cache8, block_table=block_table, seq_idx=seq_idx, pos=pos, c_kv=c_kv, k_rope=k_rope,
+             rope_tab=rope_tab, dev_status=dev_status):
+        _check(lib.mla_append_cache8(
+            _cache8_ptr(cache8), cache8.shape[0], tp, block_table.shape[0], mb,
+            _ptr(seq_idx, torch.int32, (T,), "seq_idx"), _ptr(pos, torch.int32, (T,), "pos"),
+            _ptr(c_kv, torch.bfloat16, (T, D_C), "c_kv"), _ptr(k_rope, torch.bfloat16, (T, D_R), "k_rope"),
+            _rope_ptr(rope_tab), rope_tab.shape[0], T, _ptr(dev_status, torch.int32, None, "dev_status"),
+            _stream(stream)))
+
+
+def read_cache8(cache8, block_table8, kv_len, cache, block_table, dev_status=None, stream=None):
+    """Bring the first kv_len[b] tokens of every sequence of an 8-bit cache back into the bf16 pool ``cache``."""
+    B = kv_len.shape[0]
+    with _on(stream, cache8=cache8, block_table8=block_table8, kv_len=kv_len, cache=cache, block_table=block_table,
+             dev_status=dev_status):
+        _check(lib.mla_read_cache8(
+            _cache8_ptr(cache8), cache8.shape[0], *_table(block_table8, B), _ptr(kv_len, torch.int32, (B,), "kv_len"),
+            B, _cache_ptr(cache), cache.shape[0], *_table(block_table, B),
+            _ptr(dev_status, torch.int32, None, "dev_status"), _stream(stream)))
+    return cache
+
+
+def decode8_workspace_bytes(B: int, n_q: int, H: int, num_splits: int = 0) -> int:
+    return int(lib.mla_decode8_workspace_bytes(B, n_q, H, num_splits))
+
+
+def decode8(q, cache8, block_table, kv_len, W_UV, n_q: int, scale: float, num_splits: int = 0,
+            workspace=None, out=None, lse_out=None, dev_status=None, stream=None):
+    """One absorbed decode step over an 8-bit cache: out bf16 [B*n_q, H, 128] (and lse fp32 [B*n_q, H] if given)."""
+    B = kv_len.shape[0]
+    T, H = q.shape[0], q.shape[1]
+    if T != B * n_q:
+        raise MLAError("q rows must equal len(kv_len) * n_q")
+    with _on(stream, q=q, cache8=cache8, block_table=block_table, kv_len=kv_len, W_UV=W_UV, workspace=workspace, out=out,
+             lse_out=lse_out, dev_status=dev_status):
+        if workspace is None:
+            workspace = torch.empty(decode8_workspace_bytes(B, n_q, H, num_splits), dtype=torch.uint8, device=q.device)
+        if out is None:
+            out = torch.empty((T, H, D_H), dtype=torch.bfloat16, device=q.device)
+        _check(lib.mla_decode8(
+            _ptr(q, torch.bfloat16, (T, H, D_ROW), "q"), _cache8_ptr(cache8), cache8.shape[0], *_table(block_table, B),
+            _ptr(kv_len, torch.int32, (B,), "kv_len"),
+            _ptr(W_UV, torch.bfloat16, (H, D_H, D_C), "W_UV"), B, n_q, H, float(scale), num_splits,
+            _ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size(),
+            _ptr(out, torch.bfloat16, (T, H, D_H), "out"), _ptr(lse_out, torch.float32, (T, H), "lse_out"),
+            _ptr(dev_status, torch.int32, None, "dev_status"), _stream(stream)))
+    return out
 
 
 def decode_workspace_bytes(B: int, n_q: int, H: int, num_splits: int = 0) -> int:

@@ -196,6 +196,70 @@ mla_status mla_append_cache(void* cache, int64_t cap_blocks, const int32_t* bloc
                                            static_cast<cudaStream_t>(stream)));
 }
 
+mla_status mla_append_cache8(void* cache8, int64_t cap_blocks, const int32_t* block_table, int num_seqs,
+                             int max_blocks, const int32_t* seq_idx, const int32_t* pos, const void* c_kv,
+                             const void* k_rope, const float* rope_table, int64_t rope_len, int T,
+                             int32_t* dev_status, mla_stream stream) {
+    if (T < 0 || cap_blocks < 0 || cap_blocks > kMaxPoolBlocks || rope_len < 0 || max_blocks < 0 || num_seqs < 0)
+        return MLA_ERR_INVALID_ARG;
+    if (T == 0) return MLA_OK;
+    if (!cache8 || !block_table || !seq_idx || !pos || !c_kv || !k_rope || !rope_table || max_blocks < 1 ||
+        num_seqs < 1)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(cache8) || !aligned16(c_kv) || !aligned16(k_rope) || !aligned16(rope_table))
+        return MLA_ERR_INVALID_ARG;
+    return cuda_status(launch_append_cache8(static_cast<uint8_t*>(cache8), cap_blocks, block_table, num_seqs,
+                                            max_blocks, seq_idx, pos, static_cast<const uint16_t*>(c_kv),
+                                            static_cast<const uint16_t*>(k_rope), rope_table, rope_len, T, dev_status,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_t* block_table8, int max_blocks8,
+                           const int32_t* kv_len, int B, void* cache, int64_t cap_blocks, const int32_t* block_table,
+                           int max_blocks, int32_t* dev_status, mla_stream stream) {
+    if (B < 0 || cap_blocks8 < 0 || cap_blocks8 > kMaxPoolBlocks || cap_blocks < 0 || cap_blocks > kMaxPoolBlocks ||
+        max_blocks8 < 0 || max_blocks8 > kMaxTableBlocks || max_blocks < 0 || max_blocks > kMaxTableBlocks)
+        return MLA_ERR_INVALID_ARG;
+    if (B == 0) return MLA_OK;
+    if (!cache8 || !block_table8 || !kv_len || !cache || !block_table || max_blocks8 < 1 || max_blocks < 1 ||
+        cap_blocks8 < 1 || cap_blocks < 1)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(cache8) || !aligned16(cache)) return MLA_ERR_INVALID_ARG;
+    return cuda_status(launch_read_cache8(static_cast<const uint8_t*>(cache8), cap_blocks8, block_table8, max_blocks8,
+                                          kv_len, B, static_cast<uint8_t*>(cache), cap_blocks, block_table, max_blocks,
+                                          dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits) {
+    if (B < 1) return 0;
+    return mla_decode_cudacore_workspace_bytes(B, n_q, H, num_splits);
+}
+
+mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, const int32_t* block_table,
+                       int max_blocks, const int32_t* kv_len, const void* W_UV, int B, int n_q, int H, float scale,
+                       int num_splits, void* workspace, size_t ws_bytes, void* out, float* lse_out,
+                       int32_t* dev_status, mla_stream stream) {
+    mla_status st = check_decode_shape(B, cap_blocks, max_blocks, n_q, H, num_splits);
+    if (st != MLA_OK) return st;
+    if (!(scale > 0.f) || !isfinite(scale)) return MLA_ERR_INVALID_ARG;
+    if (B == 0) return MLA_OK;
+    if (!q || !cache8 || !block_table || !kv_len || !W_UV || !out || !workspace) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache8) || !aligned16(W_UV) || !aligned16(out) || !aligned16(workspace))
+        return MLA_ERR_INVALID_ARG;
+    const int S = num_splits ? num_splits : auto_splits(B, n_q, H);
+    const DecodeWs lay = decode_ws_layout(B, n_q, H, S);
+    if (ws_bytes < lay.total) return MLA_ERR_WORKSPACE;
+    float* o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lay.o_part);
+    float* lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lay.lse_part);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_decode8_simt(static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(cache8),
+                                        cap_blocks, block_table, max_blocks, kv_len, B, n_q, H, scale, S, o_part,
+                                        lse_part, dev_status, cs);
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    return cuda_status(launch_combine(o_part, lse_part, B * n_q, H, S, static_cast<const uint16_t*>(W_UV), out,
+                                      lse_out, cs, true));
+}
+
 size_t mla_decode_workspace_bytes(int B, int n_q, int H, int num_splits) {
     if (B < 0 || n_q < 1 || H < 1 || num_splits < 0) return 0;
     return tc_ws_layout(B, n_q, H).total;

@@ -19,6 +19,13 @@ constexpr int kBlockTokens = MLA_BLOCK_TOKENS;  // tokens per cache block
 constexpr int kBlockBytes = MLA_BLOCK_BYTES;    // 9 chunks x [128 rows x 128 B]
 constexpr int kBlockChunk = kBlockTokens * 128;  // bytes of one 64-column chunk of a block
 static_assert(kBlockBytes == 9 * kBlockChunk, "block layout");
+// 8-bit cache block: four 16 KB latent chunks of 128 columns, the RoPE columns (64 bytes a row), the scales.
+constexpr int kBlock8Bytes = MLA_BLOCK8_BYTES;
+constexpr int kBlock8Chunk = kBlockTokens * 128;
+constexpr int kBlock8Rope = 4 * kBlock8Chunk;
+constexpr int kBlock8Scales = kBlock8Rope + kBlockTokens * kDr;
+static_assert(kBlock8Bytes == kBlock8Scales + kBlockTokens * 4, "8-bit block layout");
+constexpr int kScale8MinExp = -40;  // smallest scale of a row: 2^-40
 constexpr int kMaxPairs = 74;      // CTA pairs per row group the tensor-core decode uses at most (148 SMs / 2)
 constexpr int kMaxSmRows = 32;     // query rows (n_q * H) up to which the one-SM decode kernel runs instead
 constexpr int kMaxSmCtas = 148;    // CTAs the one-SM decode kernel uses at most (one per SM)
@@ -35,6 +42,12 @@ __host__ __device__ __forceinline__ int valid_seq_tiles(int L, int n_q, int max_
 // Byte offset of column c of row r inside a cache block (128-byte swizzle per 64-column chunk).
 __host__ __device__ __forceinline__ int block_offset(int r, int c) {
     return (c >> 6) * kBlockChunk + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
+}
+
+// Byte offset of column c of row r inside a block of the 8-bit cache.
+__host__ __device__ __forceinline__ int block8_offset(int r, int c) {
+    return c < kDc ? (c >> 7) * kBlock8Chunk + r * 128 + ((((c & 127) >> 4) ^ (r & 7)) << 4) + (c & 15)
+                   : kBlock8Rope + r * 64 + ((((c - kDc) >> 4) ^ ((r >> 1) & 3)) << 4) + (c & 15);
 }
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
@@ -64,6 +77,15 @@ cudaError_t launch_append_cache(uint8_t* cache, int64_t cap_blocks, const int32_
                                 const uint16_t* k_rope, const float* rope_table, int64_t rope_len, int T,
                                 int32_t* dev_status, cudaStream_t stream);
 
+// The 8-bit cache: quantised append and read-back (cache8.cu).
+cudaError_t launch_append_cache8(uint8_t* cache, int64_t cap_blocks, const int32_t* block_table, int num_seqs,
+                                 int max_blocks, const int32_t* seq_idx, const int32_t* pos, const uint16_t* c_kv,
+                                 const uint16_t* k_rope, const float* rope_table, int64_t rope_len, int T,
+                                 int32_t* dev_status, cudaStream_t stream);
+cudaError_t launch_read_cache8(const uint8_t* cache8, int64_t cap8, const int32_t* table8, int mb8,
+                               const int32_t* kv_len, int B, uint8_t* cache, int64_t cap, const int32_t* table, int mb16,
+                               int32_t* dev_status, cudaStream_t stream);
+
 cudaError_t launch_absorb_tc(const uint16_t* q_nope, const uint16_t* q_rope, const int32_t* pos, const uint16_t* W_UK,
                              const float* rope_table, int64_t rope_len, int T, int H, uint16_t* q_out,
                              int32_t* dev_status, cudaStream_t stream);
@@ -89,8 +111,13 @@ cudaError_t launch_decode_simt(const uint16_t* q, const uint8_t* cache, int64_t 
                                int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int splits,
                                float* o_part, float* lse_part, int32_t* dev_status, cudaStream_t stream);
 
+cudaError_t launch_decode8_simt(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
+                                int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int splits,
+                                float* o_part, float* lse_part, int32_t* dev_status, cudaStream_t stream);
+
 cudaError_t launch_combine(const float* o_part, const float* lse_part, int T, int H, int splits,
-                           const uint16_t* W_UV, void* out, float* lse_out, cudaStream_t stream);
+                           const uint16_t* W_UV, void* out, float* lse_out, cudaStream_t stream,
+                           bool nan_lse = false);  // nan_lse: a NaN sum gives lse = NaN, not -inf
 
 // Tensor-core decode (decode_tc.cu); the merge of its pieces and the W^UV projection (proj_tc.cu).
 int decode_tc_clusters();

@@ -212,6 +212,28 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     return r;
 }
 
+// Two fp32 -> two e4m3 (lo in bits 0..7), round to nearest even, saturating; NaN stays NaN.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 -> two fp16 (exact), packed.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
+    return r;
+}
+// Two e4m3 -> two fp32 (exact).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t codes) {
+    const uint32_t h = e4m3x2_to_f16x2(codes);
+    float2 v;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(h));
+    return v;
+}
+
 // ----------------------------------------------------------------- proxies / DSMEM
 
 __device__ __forceinline__ void fence_proxy_async_cta() {
