@@ -51,7 +51,7 @@ __device__ void up_project_block(const float (*ol)[kDc], int nt, int t0, int h, 
 
 __global__ void __launch_bounds__(256) combine_kernel(
     const float* __restrict__ o_part, const float* __restrict__ lse_part, int T, int H, int S,
-    const uint16_t* __restrict__ W_UV, void* __restrict__ out, float* __restrict__ lse_out, bool nan_lse) {
+    const uint16_t* __restrict__ W_UV, void* __restrict__ out, float* __restrict__ lse_out) {
     __shared__ float ol[kCombTok][kDc];
     const int h = blockIdx.x;
     const int t0 = blockIdx.y * kCombTok;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) combine_kernel(
         const float inv = (z > 0.f) ? 1.f / z : 0.f;
         ol[t][2 * tid] = o0 * inv;
         ol[t][2 * tid + 1] = o1 * inv;
-        if (tid == 0 && lse_out) lse_out[th] = (z > 0.f || (nan_lse && z != z)) ? m + logf(z) : -CUDART_INF_F;
+        if (tid == 0 && lse_out) lse_out[th] = (z > 0.f) ? m + logf(z) : -CUDART_INF_F;
     }
     if (W_UV == nullptr) {
         float* of = static_cast<float*>(out);
@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(256) combine_kernel(
 }
 
 cudaError_t launch_combine(const float* o_part, const float* lse_part, int T, int H, int splits,
-                           const uint16_t* W_UV, void* out, float* lse_out, cudaStream_t stream, bool nan_lse) {
+                           const uint16_t* W_UV, void* out, float* lse_out, cudaStream_t stream) {
     dim3 grid(H, (T + kCombTok - 1) / kCombTok);
-    combine_kernel<<<grid, 256, 0, stream>>>(o_part, lse_part, T, H, splits, W_UV, out, lse_out, nan_lse);
+    combine_kernel<<<grid, 256, 0, stream>>>(o_part, lse_part, T, H, splits, W_UV, out, lse_out);
     return cudaGetLastError();
 }
 

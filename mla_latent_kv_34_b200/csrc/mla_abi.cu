@@ -82,6 +82,23 @@ int tc_clusters_per_group(int G, int num_splits, bool one_sm) {
     return pg < max_pairs_per_group(G) ? pg : max_pairs_per_group(G);
 }
 
+// Decode over the 8-bit cache: work units per group of 128 query rows, and the same workspace regions.  Units do not
+// wait on one another, so their number need not be what the device holds at once.
+int units8(int n_q, int H) { return max_pairs_per_group((n_q * H + 127) / 128); }
+
+TcWs ws8_layout(int B, int n_q, int H) {
+    TcWs w;
+    w.G = (n_q * H + 127) / 128;
+    w.slots = B + units8(n_q, H);
+    w.rs = 128;
+    const size_t rows = static_cast<size_t>(w.G) * w.slots * w.rs;
+    w.ml_part = 0;
+    w.o_part = align1k(rows * sizeof(float2));
+    w.olat = align1k(w.o_part + rows * kDc * sizeof(float));
+    w.total = w.olat + static_cast<size_t>(H) * olat_rows(B * n_q) * 1024;
+    return w;
+}
+
 constexpr int64_t kMaxPoolBlocks = 0x7FFFFFFF;                 // block-table entries are int32
 constexpr int kMaxTableBlocks = 0x7FFFFFFF / kBlockTokens;      // positions are int32
 
@@ -231,8 +248,8 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
 }
 
 size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits) {
-    if (B < 1) return 0;
-    return mla_decode_cudacore_workspace_bytes(B, n_q, H, num_splits);
+    if (B < 1 || n_q < 1 || H < 1 || num_splits < 0) return 0;
+    return ws8_layout(B, n_q, H).total;
 }
 
 mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, const int32_t* block_table,
@@ -246,18 +263,25 @@ mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, co
     if (!q || !cache8 || !block_table || !kv_len || !W_UV || !out || !workspace) return MLA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(cache8) || !aligned16(W_UV) || !aligned16(out) || !aligned16(workspace))
         return MLA_ERR_INVALID_ARG;
-    const int S = num_splits ? num_splits : auto_splits(B, n_q, H);
-    const DecodeWs lay = decode_ws_layout(B, n_q, H, S);
+    const TcWs lay = ws8_layout(B, n_q, H);
     if (ws_bytes < lay.total) return MLA_ERR_WORKSPACE;
-    float* o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lay.o_part);
-    float* lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + lay.lse_part);
+    int units = units8(n_q, H);
+    if (num_splits > 0 && num_splits < units) units = num_splits;
+    char* ws = static_cast<char*>(workspace);
+    float* o_part = reinterpret_cast<float*>(ws + lay.o_part);
+    float2* ml_part = reinterpret_cast<float2*>(ws + lay.ml_part);
+    uint8_t* olat = reinterpret_cast<uint8_t*>(ws + lay.olat);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_decode8_simt(static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(cache8),
-                                        cap_blocks, block_table, max_blocks, kv_len, B, n_q, H, scale, S, o_part,
-                                        lse_part, dev_status, cs);
-    if (e != cudaSuccess) return MLA_ERR_CUDA;
-    return cuda_status(launch_combine(o_part, lse_part, B * n_q, H, S, static_cast<const uint16_t*>(W_UV), out,
-                                      lse_out, cs, true));
+    cudaError_t e = launch_decode8_tc(static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(cache8), cap_blocks,
+                                      block_table, max_blocks, kv_len, B, n_q, H, scale, units, o_part, ml_part,
+                                      lay.slots, dev_status, cs);
+    if (e == cudaSuccess)
+        e = launch_merge(o_part, ml_part, kv_len, max_blocks, B, n_q, H, units, lay.slots, lay.rs, olat, lse_out,
+                         dev_status, cs, true);
+    if (e == cudaSuccess)
+        e = launch_upproj(olat, static_cast<const uint16_t*>(W_UV), B * n_q, H, static_cast<uint16_t*>(out), dev_status,
+                          cs);
+    return cuda_status(e);
 }
 
 size_t mla_decode_workspace_bytes(int B, int n_q, int H, int num_splits) {

@@ -111,13 +111,8 @@ cudaError_t launch_decode_simt(const uint16_t* q, const uint8_t* cache, int64_t 
                                int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int splits,
                                float* o_part, float* lse_part, int32_t* dev_status, cudaStream_t stream);
 
-cudaError_t launch_decode8_simt(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
-                                int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int splits,
-                                float* o_part, float* lse_part, int32_t* dev_status, cudaStream_t stream);
-
 cudaError_t launch_combine(const float* o_part, const float* lse_part, int T, int H, int splits,
-                           const uint16_t* W_UV, void* out, float* lse_out, cudaStream_t stream,
-                           bool nan_lse = false);  // nan_lse: a NaN sum gives lse = NaN, not -inf
+                           const uint16_t* W_UV, void* out, float* lse_out, cudaStream_t stream);
 
 // Tensor-core decode (decode_tc.cu); the merge of its pieces and the W^UV projection (proj_tc.cu).
 int decode_tc_clusters();
@@ -130,6 +125,10 @@ cudaError_t launch_decode_tc(const uint16_t* q, const uint8_t* cache, int64_t ca
                              int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale,
                              int clusters_per_group, float* o_part, float2* ml_part, int slots, int32_t* dev_status,
                              cudaStream_t stream);
+// Attend phase over the 8-bit cache (decode8_tc.cu): P_g CTA pairs per group of 128 query rows.
+cudaError_t launch_decode8_tc(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
+                              int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int P_g,
+                              float* o_part, float2* ml_part, int slots, int32_t* dev_status, cudaStream_t stream);
 // Rows of the merged latent output o_lat kept for the up-projection: T rounded so that every 64-token
 // block but the last is full and the last is a multiple of 16 (the MMA N granularity).
 __host__ __device__ __forceinline__ int olat_rows(int T) {
@@ -138,7 +137,8 @@ __host__ __device__ __forceinline__ int olat_rows(int T) {
 }
 cudaError_t launch_merge(const float* o_part, const float2* ml_part, const int32_t* kv_len, int max_blocks, int B,
                          int n_q, int H, int P_g, int slots, int rs, uint8_t* olat, float* lse_out,
-                         int32_t* dev_status, cudaStream_t stream);
+                         int32_t* dev_status, cudaStream_t stream,
+                         bool nan_lse = false);  // nan_lse: a row whose sum is NaN gets lse = NaN, not -inf
 cudaError_t launch_upproj(const uint8_t* olat, const uint16_t* W_UV, int T, int H, uint16_t* out, int32_t* dev_status,
                           cudaStream_t stream);
 
