@@ -1,12 +1,14 @@
 // What the two attend kernels of the 8-bit cache share: the split of the (sequence, tile) space into pieces, the
 // block lookup, and the two-term e4m3 form of queries and probabilities.
 //
-// Two terms.  The tensor cores multiply e4m3 by e4m3, so the codes of the cache go into them as they stand.  The other
-// operand, a bf16 query or an fp32 probability, is written as hi + lo, both e4m3: hi holds 4 significant bits, lo the
-// next 4 of what is left.  A bf16 value (8 significant bits) is represented exactly as long as its last bit is at
+// Two terms.  The tensor cores multiply 8-bit values, so the codes of the cache go into them as they stand.  The other
+// operand, a bf16 query or an fp32 probability, is written as hi + lo: hi (e4m3) holds 4 significant bits, lo what is
+// left.  For the query lo is e4m3 too, the next 4 bits: a bf16 value (8 significant bits) is represented exactly as long as its last bit is at
 // least 2^-9 (the e4m3 step near 0); scaled by a power of two so that the row's largest value lies in (224, 448], that
 // is every element down to 2^-10 of the largest, and an absolute 2^-19 of the largest below.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "mla_internal.cuh"
 #include "sm100.cuh"
@@ -157,50 +159,93 @@ __device__ __forceinline__ void split4_q(uint32_t w0, uint32_t w1, float inv, ui
     lo = l0 | (static_cast<uint32_t>(l1) << 16);
 }
 
-// hi part of a probability 0 <= p <= 2^8.75: p rounded to 4 significant bits (half up), still fp32.  p - hi is exact.
-__device__ __forceinline__ float hi_part(float p) {
-    return __uint_as_float((__float_as_uint(p) + 0x00080000u) & 0xFFF00000u);
+// Packed fp32 arithmetic (two lanes an instruction).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 c, a, b;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// The lower byte to add to each fp16 of a pair before its upper byte is taken: half a step (rounding to nearest) where
+// the probability is at least 2^-6, the given dither where it is smaller.
+__device__ __forceinline__ uint32_t round_bytes(uint32_t p01, uint32_t dither) {
+    const __half2 least = __halves2half2(__ushort_as_half(0x2400), __ushort_as_half(0x2400));  // 2^-6
+    const uint32_t small = __hlt2_mask(*reinterpret_cast<const __half2*>(&p01), least);
+    return (small & dither) | (~small & 0x00800080u);
+}
+
+// Four probabilities 0 <= p <= 2^8.75 as hi (e4m3) and lo (e5m2) codes.  hi rounds to nearest; lo is what is left, in
+// e5m2's 3 significant bits: e5m2 is the upper half of an fp16, so an integer addition to the lower byte rounds it.  Down
+// to p = 2^-6 the pair holds p within 2^-8, like a bf16.  Below, hi's steps are 2^-9 and lo goes on to 2^-16; there the
+// rounding is dithered, over the tokens alike, so that many equal small probabilities (a long tail behind one dominant
+// token) keep their sum, which rounding to nearest would move by up to an eighth.
+__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t dither01, uint32_t dither23,
+                                         uint32_t& hi, uint32_t& lo) {
+    uint32_t h01, h23, d01, d23;
+    uint16_t a, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h23) : "f"(p3), "f"(p2));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h01));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(h23));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d01) : "r"(h01), "r"(e4m3x2_to_f16x2(a)));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
+    hi = a | (static_cast<uint32_t>(b) << 16);
+    lo = __byte_perm(d01 + round_bytes(h01, dither01), d23 + round_bytes(h23, dither23), 0x7531);
+}
+// The dither of token pair k of a thread's row part: two bytes of a low-discrepancy sequence (multiples of the golden
+// ratio), one in each half's lower byte.
+__host__ __device__ constexpr uint32_t dither_pair(int k) {
+    return ((static_cast<uint32_t>(2 * k) * 40503u + 20251u >> 8) & 0xFFu) |
+           (((static_cast<uint32_t>(2 * k + 1) * 40503u + 20251u >> 8) & 0xFFu) << 16);
 }
 
 // The reference exponent of a row's probabilities, P' = 2^(y - R) with y = log2(p s_t) (s_t, the token's scale, is
 // folded into P because V's rows are codes).  O and the sum are kept relative to R, an integer, so moving it multiplies
-// them by an exact power of two.  P' has to stay below 448 (e4m3) and its largest values well above the smallest step:
-//   up    when a tile's largest y - R exceeds 8.75;
-//   down  when it is below 5 and what came before is small too (`mass`, the sum over earlier tiles of their largest P',
-//         below 32 a tile): then the steps of 2^-9 could add up to more than 2^-8 of the row's sum.
-// Either way R is put where the tile's largest P' lies in (2^5, 2^6].  It does not go further down than 2^32 below its
-// highest place: what is that small no longer counts.
+// them by an exact power of two.  P' has to stay below 448 (e4m3): R moves up when a tile's largest y - R exceeds 8.75,
+// and then (as at a piece's first tile) to where the largest P' lies in (1, 2].  It need not move down: a probability
+// 2^-20 of the largest is still held by split4_p, and 2^17 tokens below that are less than 1/8 of the sum.
 struct RowRef {
-    float R, high, mass;
-    __device__ __forceinline__ void reset() {
-        R = __uint_as_float(0xFF800000u);
-        high = R;
-        mass = 0.f;
-    }
-    // Takes a tile's largest y (-inf: nothing visible) and the tiles before it; returns the exponent by which O and
-    // the sum are to be multiplied (<= -126: they vanish), 0 for none.
-    __device__ __forceinline__ int move(float top, int tiles_before) {
+    float R;
+    __device__ __forceinline__ void reset() { R = __uint_as_float(0xFF800000u); }
+    // Takes a tile's largest y (-inf: nothing visible); returns the exponent by which O and the sum are to be multiplied
+    // (<= -126: they vanish), 0 for none.
+    __device__ __forceinline__ int move(float top) {
         int d = 0;
-        if (top > R + 8.75f || (top < R + 5.f && top != __uint_as_float(0xFF800000u) && mass < 32.f * tiles_before)) {
-            float to = ceilf(top) - 6.f;
-            to = fmaxf(to, high - 32.f);
-            if (to != R) {
-                // (no O yet: R is -inf, and nothing is multiplied)
-                d = (R == __uint_as_float(0xFF800000u)) ? 0 : static_cast<int>(fmaxf(fminf(R - to, 126.f), -127.f));
-                R = to;
-                high = fmaxf(high, to);
-            }
+        if (top > R + 8.75f) {
+            const float to = ceilf(top) - 1.f;
+            // (no O yet: R is -inf, and nothing is multiplied)
+            d = (R == __uint_as_float(0xFF800000u)) ? 0 : static_cast<int>(fmaxf(R - to, -127.f));
+            R = to;
         }
-        mass = mass * factor(d) + (R == __uint_as_float(0xFF800000u) ? 0.f : ex2_approx(top - R));
         return d;
     }
     __device__ __forceinline__ static float factor(int d) { return d <= -126 ? 0.f : exp2_int(d); }
     __device__ __forceinline__ float minus() const { return R == __uint_as_float(0xFF800000u) ? 0.f : -R; }
 };
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A/B and fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
-    return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(b_mn_major) << 16) |
+// Instruction descriptor for kind::f8f6f4 with e4m3 operands (a_e5m2, b_e5m2: that one e5m2) and fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false,
+                                                    bool b_e5m2 = false) {
+    return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) | (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(b_mn_major) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 

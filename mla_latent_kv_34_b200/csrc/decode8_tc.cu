@@ -50,18 +50,20 @@ constexpr uint32_t kColQ = 0;     // S CTA: latent Q codes, four to a column: hi
 constexpr uint32_t kColS0 = 256;  // S CTA: two 128-column score buffers
 __device__ __forceinline__ uint32_t col_s(uint32_t sb) { return kColS0 + 128u * sb; }
 
-// shared memory, S CTA.  Staging buffer 1 shares its space with the Q transpose tiles; barriers and one buffer of token
-// scales sit in the gap behind staging buffer 0.
+// shared memory, S CTA.  Staging buffer 1 shares its space with the Q transpose tiles; barriers, the token scales and
+// one block of the exchange sit in the gap behind staging buffer 0.
 constexpr int kSOffRing = 0;                           // two tiles
 constexpr int kSOffQR = 2 * kTileBytes;                // RoPE part of Q: [128 rows x (hi 64 | lo 64)] swizzled, 16 KB
 constexpr int kSOffStage0 = kSOffQR + kRows * 128;
-constexpr int kSOffScale = kSOffStage0 + kMsgBytes;    // 128 words (scale and its exponent), tiles of even index
-constexpr int kSOffBar = kSOffScale + kTile * 4;
+constexpr int kSOffScale = kSOffStage0 + kMsgBytes;    // the tile's 128 token scales s
+constexpr int kSOffX7 = kSOffScale + kTile * 4;        // exchange block 7
+constexpr int kSOffBar = kSOffX7 + 128;
 constexpr int kSOffQT = kSOffStage0 + kMsgStride;      // 8 warps x [32 rows x 128 B] transpose tiles
 constexpr int kSOffStage1 = kSOffQT;
-constexpr int kSOffScale1 = kSOffStage1 + kMsgBytes;   // the same words, tiles of odd index
-constexpr int kSOffXchg = kSOffScale1 + kTile * 4;     // [2][128] fp32 half-row maxima / sums
-constexpr int kSEnd = kSOffXchg + 2 * kRows * 4;
+constexpr int kSOffExp = kSOffStage1 + kMsgBytes;      // log2 s
+constexpr int kSOffInv = kSOffExp + kTile * 4;         // 1 / s
+constexpr int kSOffXchg = kSOffInv + kTile * 4;        // exchange blocks 0..6: a warp's 32 half-row maxima or sums
+constexpr int kSEnd = kSOffXchg + 7 * 128;
 constexpr int kSBarFull = 0, kSBarEmpty = 4, kSBarSFull = 8, kSBarSEmpty = 10, kSBarPEmpty = 12,
               kSBarQReady = kSBarPEmpty + kPSlots, kSBarFin = kSBarQReady + 1, kSNumBars = kSBarFin + 1;
 constexpr int kSOffTail = kSOffBar + kSNumBars * 8;
@@ -80,7 +82,7 @@ static_assert(kSOffTail + kTailBytes <= kSOffQT, "barriers and tail fit the gap 
 static_assert(kSOffQR % 1024 == 0 && kSOffStage0 % 1024 == 0 && kSOffStage1 % 1024 == 0 && kOOffMsg % 1024 == 0 &&
                   kMsgStride % 1024 == 0 && kTileBytes % 1024 == 0,
               "swizzle atoms 1024-aligned");
-static_assert(kOOffBar % 8 == 0 && kSOffBar % 8 == 0 && kSOffScale % 16 == 0 && kSOffScale1 % 16 == 0, "alignment");
+static_assert(kOOffBar % 8 == 0 && kSOffBar % 8 == 0 && kSOffScale % 16 == 0 && kSOffExp % 16 == 0, "alignment");
 static_assert(kMsgBytes % 16 == 0 && kSoftWarps * 32 * 128 <= kPBytes, "bulk copy size; transpose tiles");
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t peer_abort, int32_t* dev_status) {
@@ -89,24 +91,18 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t p
     if (dev_status) atomicOr(dev_status, MLA_DEVERR_TIMEOUT);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float fmax64(const float (&v)[64]) {
-    float a = fmaxf(v[0], v[1]), b = fmaxf(v[2], v[3]), c = fmaxf(v[4], v[5]), d = fmaxf(v[6], v[7]);
+    float a = v[0], b = v[1], c = v[2], d = v[3];
 #pragma unroll
-    for (int k = 8; k < 64; k += 4) {
-        a = fmaxf(a, v[k]);
-        b = fmaxf(b, v[k + 1]);
-        c = fmaxf(c, v[k + 2]);
-        d = fmaxf(d, v[k + 3]);
+    for (int k = 4; k < 60; k += 8) {
+        a = max3(a, v[k], v[k + 1]);
+        b = max3(b, v[k + 2], v[k + 3]);
+        c = max3(c, v[k + 4], v[k + 5]);
+        d = max3(d, v[k + 6], v[k + 7]);
     }
-    return fmaxf(fmaxf(a, b), fmaxf(c, d));
+    return max3(max3(a, b, c), max3(d, v[60], v[61]), fmaxf(v[62], v[63]));
 }
-
-// A token's scale s = 2^k and its exponent, both exact in bf16, as one word: s in the upper half, k in the lower.
-__device__ __forceinline__ uint32_t scale_word(uint32_t s_bits) {
-    const float k = static_cast<float>(static_cast<int>((s_bits >> 23) & 0xFFu) - 127);
-    return (s_bits & 0xFFFF0000u) | (__float_as_uint(k) >> 16);
-}
-constexpr uint32_t kUnitScale = 0x3F800000u;  // scale_word of 1
 
 __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -214,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             }
         } else if (warp == kWarpMma) {
             // ---- MMA issuer (one thread): S[sb] = (Q_hi + Q_lo) K^T
-            if (lane == 0) {
-                constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kTile, false, false);
+            if (elect_one()) {
+                constexpr uint32_t idesc = idesc_f8_f32(kRows, kTile, false, false);
                 const uint64_t ring_desc = sdesc_sw128(sbase + kSOffRing, 16, 1024);
                 const uint64_t rope_desc = sdesc_sw64(sbase + kSOffRing + kBlock8Rope, 16, 512);
                 const uint64_t qr_desc = sdesc_sw128(sbase + kSOffQR, 16, 1024);
@@ -231,11 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
                         const uint32_t d = tmem + col_s(sb);
                         const uint64_t tile_off = static_cast<uint64_t>(sb * kTileBytes) >> 4;
+#pragma unroll 1
                         for (int k = 0; ok && k < 2; ++k) {
                             ok = mbar_wait(&bars[kSBarFull + 2 * sb + k], us & 1u, abort_flag, kLimitNs);
                             if (!ok) break;
                             tc_fence_after();
-#pragma unroll
+                            // rolled: code that fits the instruction cache beside the softmax warps' (fully unrolled, the
+                            // issue of a tile's 36 MMAs took longer than their 2304 cycles)
+#pragma unroll 1
                             for (int j = 0; j < 2; ++j) {
                                 const int c = 2 * k + j;
                                 const uint64_t cd = ring_desc + tile_off + (static_cast<uint64_t>(c * kChunk) >> 4);
@@ -269,7 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             const int qd = warp & 3, hf = warp >> 2;
             const int r = 32 * qd + lane;
             const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
-            float* xchg = reinterpret_cast<float*>(smem + kSOffXchg);  // [2][128]
+            // exchange with the warp of the same rows' other half: block 4 hf + qd (the last one apart)
+            auto xblock = [&](int h) {
+                const int i = 4 * h + qd;
+                return reinterpret_cast<float*>(smem + (i < 7 ? kSOffXchg + 128 * i : kSOffX7)) + lane;
+            };
+            volatile float* xmine = xblock(hf);
+            volatile float* xother = xblock(hf ^ 1);
             const int rr = g * kRows + r;
             const bool row_ok = rr < p.R;
             const int j = row_ok ? rr / p.H : 0;
@@ -292,28 +297,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 auto scale_bits = [&](int32_t e, int t) {
                     return (hf == 0 && t < s.t1 && t * kTile + r < s.L)
                                ? reinterpret_cast<const uint32_t*>(block_of(p, e, false) + kBlock8Scales)[r]
-                               : kUnitScale;
+                               : 0x3F800000u;
+                };
+                auto put_scale = [&](uint32_t bits) {  // s = 2^k, k, 2^-k
+                    reinterpret_cast<uint32_t*>(smem + kSOffScale)[r] = bits;
+                    reinterpret_cast<float*>(smem + kSOffExp)[r] = static_cast<float>(static_cast<int>(bits >> 23) - 127);
+                    reinterpret_cast<uint32_t*>(smem + kSOffInv)[r] = 0x7F000000u - bits;
                 };
                 const int32_t e0 = entry(s.t0), e1 = entry(s.t0 + 1);
                 int32_t e2 = entry(s.t0 + 2);
                 // this segment's query rows, two e4m3 terms each: latent part -> TMEM (warps of hf = 0: columns 0..255
                 // of a row, hf = 1: 256..511), RoPE part -> shared memory.  The warp loads its 32 rows coalesced (a
                 // lane per 16-byte unit) and transposes each 64-column chunk through a swizzled 4 KB tile into the
-                // lane-per-row order of tcgen05.st.
+                // lane-per-row order of tcgen05.st.  The bf16 rows wait in the score buffers (free between segments)
+                // until the row's largest magnitude is known.
                 float rowf;
                 {
                     uint8_t* qt = smem + kSOffQT + warp * (32 * 128);
                     const int lu = lane & 7, lr = lane >> 3;  // unit and row-in-quad of this lane's loads
-                    uint4 x[4][8], y[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int ri = 4 * i + lr;
-                            x[c][i] = make_uint4(0, 0, 0, 0);
-                            if (g * kRows + 32 * qd + ri < p.R)
-                                x[c][i] = reinterpret_cast<const uint4*>(p.q + (qrow0 + ri) * kRow)[8 * (4 * hf + c) + lu];
-                        }
+                    const uint32_t raw = t_lane + kColS0 + 128 * hf;
+                    uint32_t m2 = 0;
+                    uint4 y[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int ri = 8 * i + (lane >> 2);
@@ -321,27 +325,43 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         if (g * kRows + 32 * qd + ri < p.R)
                             y[i] = reinterpret_cast<const uint4*>(p.q + (qrow0 + ri) * kRow)[64 + 4 * hf + (lane & 3)];
                     }
-                    if (hf == 0)
-                        reinterpret_cast<uint32_t*>(smem + ((n & 1u) ? kSOffScale1 : kSOffScale))[r] =
-                            scale_word(scale_bits(e0, s.t0));
-                    // the transpose tiles double as staging buffer 1: before the first write to them, wait until the
-                    // sender has seen every copy of earlier messages read out
-                    bar_sync(kNbQFree, kSyncThreads);
-                    uint32_t m2 = 0;
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        uint4 x[2][8];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                        for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int ri = 4 * i + lr;
-                            *reinterpret_cast<uint4*>(qt + ri * 128 + ((lu ^ (ri & 7)) << 4)) = x[c][i];
+                            for (int i = 0; i < 8; ++i) {
+                                const int ri = 4 * i + lr;
+                                x[jj][i] = make_uint4(0, 0, 0, 0);
+                                if (g * kRows + 32 * qd + ri < p.R)
+                                    x[jj][i] = reinterpret_cast<const uint4*>(
+                                        p.q + (qrow0 + ri) * kRow)[8 * (4 * hf + c + jj) + lu];
+                            }
+                        if (c == 0) {
+                            if (hf == 0) put_scale(scale_bits(e0, s.t0));
+                            // the transpose tiles double as staging buffer 1: before the first write to them, wait
+                            // until the sender has seen every copy of earlier messages read out
+                            bar_sync(kNbQFree, kSyncThreads);
                         }
-                        __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            x[c][u] = *reinterpret_cast<const uint4*>(qt + lane * 128 + ((u ^ (lane & 7)) << 4));
-                            m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[c][u].x), x[c][u].y), x[c][u].z), x[c][u].w);
+                        for (int jj = 0; jj < 2; ++jj) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int ri = 4 * i + lr;
+                                *reinterpret_cast<uint4*>(qt + ri * 128 + ((lu ^ (ri & 7)) << 4)) = x[jj][i];
+                            }
+                            __syncwarp();
+                            uint32_t v[32];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const uint4 z = *reinterpret_cast<const uint4*>(qt + lane * 128 + ((u ^ (lane & 7)) << 4));
+                                v[4 * u] = z.x; v[4 * u + 1] = z.y; v[4 * u + 2] = z.z; v[4 * u + 3] = z.w;
+                                m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, z.x), z.y), z.z), z.w);
+                            }
+                            __syncwarp();
+                            tmem_st32(raw + 32 * (c + jj), v);
                         }
-                        __syncwarp();
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -355,11 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, y[u].x), y[u].y), y[u].z), y[u].w);
                     }
                     // the row's largest magnitude, over both halves of its columns
-                    uint32_t* xm = reinterpret_cast<uint32_t*>(xchg);
                     const uint32_t mine = max(m2 & 0xFFFFu, m2 >> 16);
-                    xm[hf * kRows + r] = mine;
+                    *xmine = __uint_as_float(mine);
                     bar_sync(1 + qd, 64);
-                    const uint32_t top = max(mine, xm[(hf ^ 1) * kRows + r]);
+                    const uint32_t top = max(mine, __float_as_uint(*xother));
                     const int a = top < 0x7F80u ? row_exp(top) : 0;
                     const float inv = exp2_int(-a);
                     // an infinity or NaN in the query: every score of the row is NaN
@@ -375,14 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         *reinterpret_cast<uint4*>(qr + (((2 * hf + u) ^ (r & 7)) << 4)) = hi;
                         *reinterpret_cast<uint4*>(qr + (((4 + 2 * hf + u) ^ (r & 7)) << 4)) = lo;
                     }
-#pragma unroll
+                    tmem_wait_st();
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t hi[32], lo[32];
+                        uint32_t v[32], hi[32], lo[32];
+                        tmem_ld32(raw + 32 * c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            split4_q(x[c][u].x, x[c][u].y, inv, hi[2 * u], lo[2 * u]);
-                            split4_q(x[c][u].z, x[c][u].w, inv, hi[2 * u + 1], lo[2 * u + 1]);
-                        }
+                        for (int u = 0; u < 16; ++u) split4_q(v[2 * u], v[2 * u + 1], inv, hi[u], lo[u]);
                         tmem_st16(t_lane + kColQ + 16 * (4 * hf + c), hi);
                         tmem_st16(t_lane + kColQ + 128 + 16 * (4 * hf + c), lo);
                     }
@@ -400,12 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     const uint32_t sb = n & 1u, us = n >> 1;
                     if (t == t_pf && have_next && row_ok)
                         for (int c = hf; c < 9; c += 2) prefetch_l2(nq + 128 * c);
-                    // the next tile's scales (its buffer's last readers, of tile n - 1, are past that tile's barriers)
-                    if (hf == 0)
-                        reinterpret_cast<uint32_t*>(smem + ((n & 1u) ? kSOffScale : kSOffScale1))[r] = scale_word(sc1);
-                    sc1 = scale_bits(e2, t + 2);
-                    e2 = entry(t + 3);
-                    const uint4* scw = reinterpret_cast<const uint4*>(smem + ((n & 1u) ? kSOffScale1 : kSOffScale)) + 16 * hf;
                     bool ok = mbar_wait(&bars[kSBarSFull + sb], us & 1u, abort_flag, kLimitNs);
                     __syncwarp();
                     tc_fence_after();
@@ -424,46 +437,55 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     tc_fence_before();
                     mbar_arrive(&bars[kSBarSEmpty + sb]);
                     // y = log2(p s_t), before the reference: S s_t (2^a scale log2 e) + log2 s_t
+                    const float4* sc4 = reinterpret_cast<const float4*>(smem + kSOffScale) + 16 * hf;
+                    const float4* ex4 = reinterpret_cast<const float4*>(smem + kSOffExp) + 16 * hf;
+                    const float4* in4 = reinterpret_cast<const float4*>(smem + kSOffInv) + 16 * hf;
+                    const float2 rowf2 = make_float2(rowf, rowf);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const uint4 sw = scw[k];
-                        const uint32_t ws[4] = {sw.x, sw.y, sw.z, sw.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            y[4 * k + i] = fmaf(y[4 * k + i] * __uint_as_float(ws[i] & 0xFFFF0000u), rowf,
-                                                __uint_as_float(ws[i] << 16));
+                        const float4 sv = sc4[k], ev = ex4[k];
+                        const float2 y0 = fma2(mul2(make_float2(y[4 * k], y[4 * k + 1]), make_float2(sv.x, sv.y)), rowf2,
+                                               make_float2(ev.x, ev.y));
+                        const float2 y1 = fma2(mul2(make_float2(y[4 * k + 2], y[4 * k + 3]), make_float2(sv.z, sv.w)),
+                                               rowf2, make_float2(ev.z, ev.w));
+                        y[4 * k] = y0.x;
+                        y[4 * k + 1] = y0.y;
+                        y[4 * k + 2] = y1.x;
+                        y[4 * k + 3] = y1.y;
                     }
                     const int nvalid = lim - t * kTile - 64 * hf;  // columns < nvalid are visible
                     if (nvalid < 64) {
 #pragma unroll
                         for (int k = 0; k < 64; ++k) y[k] = k < nvalid ? y[k] : -CUDART_INF_F;
                     }
-                    xchg[hf * kRows + r] = fmax64(y);
+                    const float half_top = fmax64(y);
+                    *xmine = half_top;
                     bar_sync(1 + qd, 64);
-                    const float top = fmaxf(xchg[r], xchg[kRows + r]);
-                    const int d = ref.move(top, t - s.t0);
-                    const float mneg = ref.minus();
-                    float lsum = 0.f;
+                    const int d = ref.move(fmaxf(half_top, *xother));
+                    const float2 mneg = make_float2(ref.minus(), ref.minus());
+                    float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const uint4 sw = scw[k];
-                        const uint32_t ws[4] = {sw.x, sw.y, sw.z, sw.w};
-                        float pv[4], ph[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            pv[i] = ex2_approx(y[4 * k + i] + mneg);
-                            lsum = fmaf(pv[i], __uint_as_float(0x7F000000u - (ws[i] & 0xFFFF0000u)), lsum);  // / s_t
-                            ph[i] = hi_part(pv[i]);
-                        }
-                        hi[k] = cvt_e4m3x2(ph[0], ph[1]) | (cvt_e4m3x2(ph[2], ph[3]) << 16);
-                        lo[k] = cvt_e4m3x2(pv[0] - ph[0], pv[1] - ph[1]) | (cvt_e4m3x2(pv[2] - ph[2], pv[3] - ph[3]) << 16);
+                        const float4 iv = in4[k];
+                        float2 p0 = add2(make_float2(y[4 * k], y[4 * k + 1]), mneg);
+                        float2 p1 = add2(make_float2(y[4 * k + 2], y[4 * k + 3]), mneg);
+                        p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
+                        p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
+                        ls0 = fma2(p0, make_float2(iv.x, iv.y), ls0);
+                        ls1 = fma2(p1, make_float2(iv.z, iv.w), ls1);
+                        split4_p(p0.x, p0.y, p1.x, p1.y, dither_pair(2 * k), dither_pair(2 * k + 1), hi[k], lo[k]);
                     }
+                    const float lsum = (ls0.x + ls0.y) + (ls1.x + ls1.y);
                     l = fmaf(l, RowRef::factor(d), lsum);
                     if (bar_red_or(kNbFail, kSyncThreads, !ok || *abort_flag != 0)) {
                         failed = true;
                         break;
                     }
+                    // every reader of this tile's scales is past them
+                    if (hf == 0) put_scale(sc1);
+                    sc1 = scale_bits(e2, t + 2);
+                    e2 = entry(t + 3);
                     // the sender has seen the copy that last used this staging buffer (tile n - 2) read it
                     bar_sync(kNbStageFree, kSyncThreads);
                     uint8_t* stage = smem + ((n & 1u) ? kSOffStage1 : kSOffStage0);
@@ -481,10 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 }
                 if (failed) break;
                 // segment result: (R, l) with l summed over both column halves; a NaN sum keeps its piece
-                if (hf == 1) xchg[kRows + r] = l;
+                if (hf == 1) *xmine = l;
                 bar_sync(1 + qd, 64);
                 if (hf == 0 && row_ok) {
-                    const float lt = l + xchg[kRows + r];
+                    const float lt = l + *xother;
                     p.ml_part[out_row_base + static_cast<int64_t>(s.slot) * kRows + r] =
                         make_float2(lt != lt ? 0.f : ref.R, lt);
                 }
@@ -532,7 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     __syncwarp();
                 }
             }
-            if (lane == 0) bulk_wait_group_read<0>();
+            if (lane == 0) {
+                bulk_wait_group_read<0>();
+                // the O CTA's last releases of its message slots arrive here: they have to land before this CTA ends
+                for (uint32_t i = (n > kPSlots ? n - kPSlots : 0); !failed && i < n; ++i)
+                    mbar_wait<true>(&bars[kSBarPEmpty + i % kPSlots], (i / kPSlots) & 1u, abort_flag, kLimitNs);
+            }
             __syncwarp();
         }
     } else if (active && rank == 1) {
@@ -565,10 +592,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
         } else if (warp == kWarpMma) {
             // ---- MMA issuer: O += (P_hi + P_lo) V (A = P, K-major SW128; B = V, MN-major SW128, 16 KB between atoms of
             //      128 columns)
-            constexpr uint32_t idesc = idesc_e4m3_f32(kRows, 256, false, true);
+            constexpr uint32_t idesc_hi = idesc_f8_f32(kRows, 256, false, true);
+            constexpr uint32_t idesc_lo = idesc_f8_f32(kRows, 256, false, true, true);
             const uint32_t peer_pempty = mapa(sbase + kSOffBar + kSBarPEmpty * 8, peer);
             const uint64_t p_desc = sdesc_sw128(sbase + kOOffMsg, 16, 1024);
             const uint64_t v_desc = sdesc_sw128(sbase + kOOffV, kChunk, 1024);
+            const bool leader = elect_one();
             SegWalk w = walk;
             Seg s;
             uint32_t n = 0, nv = 0, kseg = 0, nresc = 0;
@@ -577,31 +606,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                     const uint32_t pb = n % kPSlots, up = n / kPSlots;
                     const bool fresh = (t == s.t0);
-                    if (lane == 0) {
+                    if (leader) {
                         ok = mbar_wait<true>(&bars[kOBarPFull + pb], up & 1u, abort_flag, kLimitNs);
                         if (ok && fresh) ok = mbar_wait(&bars[kOBarOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs);
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    ok = __any_sync(0xffffffffu, ok && leader);
                     if (!ok) break;
                     const uint8_t* msg = smem + kOOffMsg + pb * kMsgStride;
                     const bool resc = __any_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(msg + kPBytes)[lane] != 0);
                     if (!fresh && resc) {
                         // some row's reference moved: have the epilogue rescale O once all earlier MMAs are done
-                        if (lane == 0) {
+                        if (leader) {
                             *resc_pb = static_cast<int>(pb);
                             mma_commit(smem_u32(&bars[kOBarODrain]));
                             mbar_arrive(&bars[kOBarRescReq]);
                             ok = mbar_wait(&bars[kOBarRescDone], nresc & 1u, abort_flag, kLimitNs);
                         }
                         ++nresc;
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
                     }
                     const int nvalid = min(kTile, s.L - t * kTile);
+#pragma unroll 1
                     for (int k = 0; k < 2; ++k, ++nv) {
                         const uint32_t st = nv % kVStages, u = nv / kVStages;
-                        if (lane == 0) ok = mbar_wait(&bars[kOBarVFull + st], u & 1u, abort_flag, kLimitNs);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (leader) ok = mbar_wait(&bars[kOBarVFull + st], u & 1u, abort_flag, kLimitNs);
+                        ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
                         uint8_t* vst = smem + kOOffV + st * kVStageBytes;
                         if (nvalid < kTile) {
@@ -615,32 +645,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             fence_proxy_async_cta();
                         }
                         __syncwarp();
-                        if (lane == 0) {
+                        if (leader) {
                             tc_fence_after();
                             const uint64_t vd = v_desc + (static_cast<uint64_t>(st * kVStageBytes) >> 4);
                             const uint64_t pd = p_desc + (static_cast<uint64_t>(pb * kMsgStride) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                mma8_ss(tmem + 256 * k, pd + 2 * kk, vd + ((kk * 4096) >> 4), idesc,
+                                mma8_ss(tmem + 256 * k, pd + 2 * kk, vd + ((kk * 4096) >> 4), idesc_hi,
                                         (fresh && kk == 0) ? 0u : 1u);
                                 mma8_ss(tmem + 256 * k, pd + ((kRows * kTile) >> 4) + 2 * kk, vd + ((kk * 4096) >> 4),
-                                        idesc, 1u);
+                                        idesc_lo, 1u);
                             }
                             mma_commit(smem_u32(&bars[kOBarVEmpty + st]));
                         }
                         __syncwarp();
                     }
                     if (!ok) break;
-                    if (lane == 0) mma_commit(peer_pempty + 8 * pb);
+                    if (leader) mma_commit(peer_pempty + 8 * pb);
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (lane == 0) mma_commit(smem_u32(&bars[kOBarOFull]));
+                if (leader) mma_commit(smem_u32(&bars[kOBarOFull]));
                 __syncwarp();
                 ++kseg;
             }
-            if (!ok && lane == 0) raise_abort(abort_flag, peer_abort, p.dev_status);
-            if (lane == 0) {
+            if (!ok && leader) raise_abort(abort_flag, peer_abort, p.dev_status);
+            if (leader) {
                 mma_commit(smem_u32(&bars[kOBarFin]));
                 mbar_wait(&bars[kOBarFin], 0, &never, kLimitNs);
             }
