@@ -239,6 +239,10 @@ struct RowRef {
         return d;
     }
     __device__ __forceinline__ static float factor(int d) { return d <= -126 ? 0.f : exp2_int(d); }
+    // The factor from one reference to another (1 where there was none: the sum is then 0).
+    __device__ __forceinline__ static float step(float from, float to) {
+        return from == __uint_as_float(0xFF800000u) ? 1.f : factor(static_cast<int>(fmaxf(from - to, -127.f)));
+    }
     __device__ __forceinline__ float minus() const { return R == __uint_as_float(0xFF800000u) ? 0.f : -R; }
 };
 

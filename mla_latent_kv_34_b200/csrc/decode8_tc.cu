@@ -32,58 +32,55 @@ using namespace d8;
 
 constexpr int kRows = 128;                        // query rows per CTA pair
 constexpr int kChunk = kBlock8Chunk;              // [128 tokens x 128 columns] of codes: 16 KB
-constexpr int kVStageBytes = 2 * kChunk;          // O CTA: a V stage = two chunks = one N = 256 column block
-constexpr int kVStages = 4;                       // two tiles
-constexpr int kPBytes = 2 * kRows * kTile;        // hi and lo chunks of [128 rows x 128 tokens]
-constexpr int kMsgBytes = kPBytes + kRows;        // P | per-row rescale exponents (int8): one bulk copy
-constexpr int kMsgStride = 33792;                 // 1024-aligned message slots
-constexpr int kPSlots = 3;
-constexpr int kSoftWarps = 8;
+constexpr int kVBytes = 4 * kChunk;               // O CTA: a V stage = the four latent chunks of a tile (two copies)
+constexpr int kVStages = 2;
+constexpr int kUnit = kTile / 4;                  // tokens of a unit: a quarter tile
+constexpr int kPBytes = kRows * 128;              // a P message: two units, [128 rows x (hi 64 tokens | lo 64 tokens)]
+constexpr int kMsgBytes = kPBytes + 2 * kRows;    // P | per unit and row the rescale exponent (int8): one bulk copy
+constexpr int kMsgStride = 17408;                 // 1024-aligned
+constexpr int kPSlots = 5;                        // O CTA: message slots
+constexpr int kStages = 3;                        // S CTA: staging buffers
+constexpr int kSoftWarps = 16;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpSender = 10;
-constexpr int kThreads = 352;
-constexpr int kSyncThreads = kSoftThreads + 32;   // softmax warps + the sender warp
-constexpr uint32_t kNbQFree = 5, kNbFail = 6, kNbStaged = 7, kNbStageFree = 8;  // named barriers (1..4: quadrant pairs)
+constexpr int kWarpProducer = 16, kWarpMma = 17, kWarpSender = 18, kWarpScale = 19;
+constexpr int kThreads = 640;
 
 // TMEM columns (512 allocated in each CTA)
 constexpr uint32_t kColQ = 0;     // S CTA: latent Q codes, four to a column: hi 0..127, lo 128..255
 constexpr uint32_t kColS0 = 256;  // S CTA: two 128-column score buffers
 __device__ __forceinline__ uint32_t col_s(uint32_t sb) { return kColS0 + 128u * sb; }
 
-// shared memory, S CTA.  Staging buffer 1 shares its space with the Q transpose tiles; barriers, the token scales and
-// one block of the exchange sit in the gap behind staging buffer 0.
+// shared memory, S CTA.  The staging buffers also hold the Q transpose tiles, while a segment's queries are loaded.
 constexpr int kSOffRing = 0;                           // two tiles
 constexpr int kSOffQR = 2 * kTileBytes;                // RoPE part of Q: [128 rows x (hi 64 | lo 64)] swizzled, 16 KB
-constexpr int kSOffStage0 = kSOffQR + kRows * 128;
-constexpr int kSOffScale = kSOffStage0 + kMsgBytes;    // the tile's 128 token scales s
-constexpr int kSOffX7 = kSOffScale + kTile * 4;        // exchange block 7
-constexpr int kSOffBar = kSOffX7 + 128;
-constexpr int kSOffQT = kSOffStage0 + kMsgStride;      // 8 warps x [32 rows x 128 B] transpose tiles
-constexpr int kSOffStage1 = kSOffQT;
-constexpr int kSOffExp = kSOffStage1 + kMsgBytes;      // log2 s
-constexpr int kSOffInv = kSOffExp + kTile * 4;         // 1 / s
-constexpr int kSOffXchg = kSOffInv + kTile * 4;        // exchange blocks 0..6: a warp's 32 half-row maxima or sums
-constexpr int kSEnd = kSOffXchg + 7 * 128;
+constexpr int kSOffStage = kSOffQR + kRows * 128;      // kStages staging buffers, kMsgStride apart
+constexpr int kScaleBufs = 4;
+constexpr int kScaleBytes = 2 * kTile * 2;             // a tile's token scales s, then log2 s, as bf16 (both exact)
+constexpr int kSOffScale = kSOffStage + kStages * kMsgStride;
+constexpr int kSOffRef = kSOffScale + kScaleBufs * kScaleBytes;  // [4][128] reference exponents handed on
+constexpr int kSOffLx = kSOffRef + 4 * kRows * 4;      // [3][2][128] a segment's (sum, R) of the first three quarters
+constexpr int kSOffBar = kSOffLx + 6 * kRows * 4;
 constexpr int kSBarFull = 0, kSBarEmpty = 4, kSBarSFull = 8, kSBarSEmpty = 10, kSBarPEmpty = 12,
-              kSBarQReady = kSBarPEmpty + kPSlots, kSBarFin = kSBarQReady + 1, kSNumBars = kSBarFin + 1;
+              kSBarFree = kSBarPEmpty + kPSlots, kSBarStaged = kSBarFree + kStages, kSBarRef = kSBarStaged + kStages,
+              kSBarQx = kSBarRef + 16, kSBarLx = kSBarQx + 4, kSBarQFree = kSBarLx + 4, kSBarQReady = kSBarQFree + 1,
+              kSBarFin = kSBarQReady + 1, kSNumBars = kSBarFin + 1;
 constexpr int kSOffTail = kSOffBar + kSNumBars * 8;
 // shared memory, O CTA
 constexpr int kOOffV = 0;
-constexpr int kOOffMsg = kVStages * kVStageBytes;
-constexpr int kOOffBar = kOOffMsg + (kPSlots - 1) * kMsgStride + kMsgBytes;
+constexpr int kOOffMsg = kVStages * kVBytes;
+constexpr int kOOffBar = kOOffMsg + kPSlots * kMsgStride;
 constexpr int kOBarVFull = 0, kOBarVEmpty = kVStages, kOBarPFull = 2 * kVStages, kOBarOFull = kOBarPFull + kPSlots,
               kOBarOFree = kOBarOFull + 1, kOBarRescReq = kOBarOFree + 1, kOBarRescDone = kOBarRescReq + 1,
               kOBarODrain = kOBarRescDone + 1, kOBarFin = kOBarODrain + 1, kONumBars = kOBarFin + 1;
 constexpr int kOOffTail = kOOffBar + kONumBars * 8;
 constexpr int kTailBytes = 32;  // tmem base, abort flag, resc slot, [tile total, first sequence, its first tile]
-constexpr int kSmemBytes = kSEnd > kOOffTail + kTailBytes ? kSEnd : kOOffTail + kTailBytes;
+constexpr int kSmemBytes = (kSOffTail > kOOffTail ? kSOffTail : kOOffTail) + kTailBytes;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kSOffTail + kTailBytes <= kSOffQT, "barriers and tail fit the gap behind staging buffer 0");
-static_assert(kSOffQR % 1024 == 0 && kSOffStage0 % 1024 == 0 && kSOffStage1 % 1024 == 0 && kOOffMsg % 1024 == 0 &&
-                  kMsgStride % 1024 == 0 && kTileBytes % 1024 == 0,
+static_assert(kSOffQR % 1024 == 0 && kSOffStage % 1024 == 0 && kOOffMsg % 1024 == 0 && kMsgStride % 1024 == 0 &&
+                  kTileBytes % 1024 == 0,
               "swizzle atoms 1024-aligned");
-static_assert(kOOffBar % 8 == 0 && kSOffBar % 8 == 0 && kSOffScale % 16 == 0 && kSOffExp % 16 == 0, "alignment");
-static_assert(kMsgBytes % 16 == 0 && kSoftWarps * 32 * 128 <= kPBytes, "bulk copy size; transpose tiles");
+static_assert(kOOffBar % 8 == 0 && kSOffBar % 8 == 0 && kSOffScale % 16 == 0, "alignment");
+static_assert(kMsgBytes % 16 == 0 && kSoftWarps * 32 * 64 <= kStages * kMsgStride, "bulk copy size; transpose tiles");
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t peer_abort, int32_t* dev_status) {
     *abort_flag = 1;
@@ -92,16 +89,14 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t p
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-__device__ __forceinline__ float fmax64(const float (&v)[64]) {
-    float a = v[0], b = v[1], c = v[2], d = v[3];
-#pragma unroll
-    for (int k = 4; k < 60; k += 8) {
-        a = max3(a, v[k], v[k + 1]);
-        b = max3(b, v[k + 2], v[k + 3]);
-        c = max3(c, v[k + 4], v[k + 5]);
-        d = max3(d, v[k + 6], v[k + 7]);
-    }
-    return max3(max3(a, b, c), max3(d, v[60], v[61]), fmaxf(v[62], v[63]));
+__device__ __forceinline__ float fmax16(const float (&v)[16]) {
+    const float a = max3(v[0], v[1], v[2]), b = max3(v[3], v[4], v[5]), c = max3(v[6], v[7], v[8]);
+    const float d = max3(v[9], v[10], v[11]), e = max3(v[12], v[13], v[14]);
+    return fmaxf(max3(a, b, c), max3(d, e, v[15]));
+}
+// Two packed bf16 as fp32.
+__device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p) {
@@ -129,10 +124,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 mbar_init(&bars[kSBarEmpty + i], 1);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&bars[kSBarSFull + i], 1);
+                mbar_init(&bars[kSBarSFull + i], 2);  // the scores' MMAs and the scales
                 mbar_init(&bars[kSBarSEmpty + i], kSoftThreads);
             }
             for (int i = 0; i < kPSlots; ++i) mbar_init(&bars[kSBarPEmpty + i], 1);
+            for (int i = 0; i < kStages; ++i) {
+                mbar_init(&bars[kSBarFree + i], 1);
+                mbar_init(&bars[kSBarStaged + i], kSoftThreads / 2);  // the eight warps of two units
+            }
+            for (int i = 0; i < 16; ++i) mbar_init(&bars[kSBarRef + i], 32);
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&bars[kSBarQx + i], 128);
+                mbar_init(&bars[kSBarLx + i], 96);
+            }
+            mbar_init(&bars[kSBarQFree], 1);
             mbar_init(&bars[kSBarQReady], kSoftThreads);
             mbar_init(&bars[kSBarFin], 1);
         } else {
@@ -140,11 +145,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 mbar_init(&bars[kOBarVFull + i], 1);
                 mbar_init(&bars[kOBarVEmpty + i], 1);
             }
-            for (int i = 0; i < kPSlots; ++i) mbar_init(&bars[kOBarPFull + i], 1);
+            // a message slot's barrier is armed here, not by the sender: a remote arrive (a release at cluster scope)
+            // held the sender up for about 2000 cycles a message
+            for (int i = 0; i < kPSlots; ++i) {
+                mbar_init(&bars[kOBarPFull + i], 1);
+                mbar_arrive_expect_tx(&bars[kOBarPFull + i], kMsgBytes);
+            }
             mbar_init(&bars[kOBarOFull], 1);
-            mbar_init(&bars[kOBarOFree], kRows);
+            mbar_init(&bars[kOBarOFree], kSoftThreads);
             mbar_init(&bars[kOBarRescReq], 1);
-            mbar_init(&bars[kOBarRescDone], kRows);
+            mbar_init(&bars[kOBarRescDone], kSoftThreads);
             mbar_init(&bars[kOBarODrain], 1);
             mbar_init(&bars[kOBarFin], 1);
         }
@@ -264,300 +274,353 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             }
             __syncwarp();
         } else if (warp < kSoftWarps) {
-            // ---- softmax: warp (qd, hf) owns TMEM lanes 32 qd.. (query rows) and score columns 64 hf .. 64 hf + 63
-            const int qd = warp & 3, hf = warp >> 2;
+            // ---- softmax: warp (qd, cq) owns TMEM lanes 32 qd.. (query rows) and the tokens 32 cq .. 32 cq + 31 of every
+            //      tile: a unit.  The units of a row follow one another only in the reference exponent, which a warp hands
+            //      on as soon as it knows its maximum; its exponentials and its part of the P message then overlap the
+            //      other warps', so nothing holds the sixteen warps in step (a barrier a tile left them waiting on one
+            //      another and on latencies half the time).
+            const int qd = warp & 3, cq = warp >> 2;
             const int r = 32 * qd + lane;
             const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
-            // exchange with the warp of the same rows' other half: block 4 hf + qd (the last one apart)
-            auto xblock = [&](int h) {
-                const int i = 4 * h + qd;
-                return reinterpret_cast<float*>(smem + (i < 7 ? kSOffXchg + 128 * i : kSOffX7)) + lane;
-            };
-            volatile float* xmine = xblock(hf);
-            volatile float* xother = xblock(hf ^ 1);
             const int rr = g * kRows + r;
             const bool row_ok = rr < p.R;
-            const int j = row_ok ? rr / p.H : 0;
+            const int gA = g * kRows + 32 * qd + (lane & 15), gB = gA + 16;
+            const int cb = 32 * cq + 16 * (lane >> 4);  // this thread's first score column
+            volatile float* ref_in = reinterpret_cast<volatile float*>(smem + kSOffRef) + ((cq + 3) & 3) * kRows + 32 * qd;
+            volatile float* ref_out = reinterpret_cast<volatile float*>(smem + kSOffRef) + cq * kRows + 32 * qd;
+            volatile float* lx = reinterpret_cast<volatile float*>(smem + kSOffLx) + 32 * qd + lane;
+            uint64_t* bar_in = &bars[kSBarRef + 4 * ((cq + 3) & 3) + qd];
+            uint64_t* bar_out = &bars[kSBarRef + 4 * cq + qd];
             SegWalk w = walk, wn;
             Seg s, sn;
-            uint32_t n = 0;
-            bool failed = false;
+            uint32_t n = 0, kseg = 0, nref = 0;  // tiles, segments, references received
+            bool ok = true;
             bool have = w.next(p, s);
-            while (!failed && have) {
+            while (ok && have) {
                 wn = w;
                 const bool have_next = wn.next(p, sn);
-                const int64_t qrow0 = static_cast<int64_t>(s.b) * p.R + g * kRows + 32 * qd;
                 const int t_pf = max(s.t0, s.t1 - 2);
                 const char* nq = (have_next && row_ok) ? reinterpret_cast<const char*>(
                                                               p.q + (static_cast<int64_t>(sn.b) * p.R + rr) * kRow)
                                                         : nullptr;
-                // token r's scale in the tiles to come (the warps of hf = 0): that of tile t + 1 and the table entry of
-                // tile t + 2 are under way while tile t is worked on
-                auto entry = [&](int t) { return (hf == 0 && t < s.t1) ? s.tab[t] : 0; };
-                auto scale_bits = [&](int32_t e, int t) {
-                    return (hf == 0 && t < s.t1 && t * kTile + r < s.L)
-                               ? reinterpret_cast<const uint32_t*>(block_of(p, e, false) + kBlock8Scales)[r]
-                               : 0x3F800000u;
-                };
-                auto put_scale = [&](uint32_t bits) {  // s = 2^k, k, 2^-k
-                    reinterpret_cast<uint32_t*>(smem + kSOffScale)[r] = bits;
-                    reinterpret_cast<float*>(smem + kSOffExp)[r] = static_cast<float>(static_cast<int>(bits >> 23) - 127);
-                    reinterpret_cast<uint32_t*>(smem + kSOffInv)[r] = 0x7F000000u - bits;
-                };
-                const int32_t e0 = entry(s.t0), e1 = entry(s.t0 + 1);
-                int32_t e2 = entry(s.t0 + 2);
-                // this segment's query rows, two e4m3 terms each: latent part -> TMEM (warps of hf = 0: columns 0..255
-                // of a row, hf = 1: 256..511), RoPE part -> shared memory.  The warp loads its 32 rows coalesced (a
-                // lane per 16-byte unit) and transposes each 64-column chunk through a swizzled 4 KB tile into the
-                // lane-per-row order of tcgen05.st.  The bf16 rows wait in the score buffers (free between segments)
-                // until the row's largest magnitude is known.
+                // this segment's query rows, two e4m3 terms each: latent columns 128 cq .. -> TMEM, RoPE columns 16 cq ..
+                // -> shared memory.  The warp loads its 32 rows coalesced (a lane per 16-byte unit) and transposes each
+                // 32-column chunk through a swizzled 2 KB tile into the lane-per-row order of tcgen05.st.  The bf16 rows
+                // wait in the score buffers (free between segments) until the row's largest magnitude is known.
                 float rowf;
                 {
-                    uint8_t* qt = smem + kSOffQT + warp * (32 * 128);
-                    const int lu = lane & 7, lr = lane >> 3;  // unit and row-in-quad of this lane's loads
-                    const uint32_t raw = t_lane + kColS0 + 128 * hf;
+                    const uint16_t* qb = p.q + (static_cast<int64_t>(s.b) * p.R + g * kRows + 32 * qd) * kRow;
+                    const int rows_here = p.R - g * kRows - 32 * qd;  // rows of this quadrant (may be <= 0)
+                    uint8_t* qt = smem + kSOffStage + warp * (32 * 64);
+                    const int lu = lane & 3, lr = lane >> 2;  // unit and row-in-eight of this lane's loads
+                    const uint32_t raw = t_lane + kColS0 + 64 * cq;
                     uint32_t m2 = 0;
-                    uint4 y[4];
+                    uint4 y[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ri = 8 * i + (lane >> 2);
+                    for (int i = 0; i < 2; ++i) {
+                        const int ri = 16 * i + (lane >> 1);
                         y[i] = make_uint4(0, 0, 0, 0);
-                        if (g * kRows + 32 * qd + ri < p.R)
-                            y[i] = reinterpret_cast<const uint4*>(p.q + (qrow0 + ri) * kRow)[64 + 4 * hf + (lane & 3)];
+                        if (ri < rows_here) y[i] = reinterpret_cast<const uint4*>(qb + ri * kRow)[64 + 2 * cq + (lane & 1)];
                     }
 #pragma unroll 1
                     for (int c = 0; c < 4; c += 2) {
-                        uint4 x[2][8];
+                        uint4 x[2][4];
 #pragma unroll
                         for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int ri = 4 * i + lr;
+                            for (int i = 0; i < 4; ++i) {
+                                const int ri = 8 * i + lr;
                                 x[jj][i] = make_uint4(0, 0, 0, 0);
-                                if (g * kRows + 32 * qd + ri < p.R)
-                                    x[jj][i] = reinterpret_cast<const uint4*>(
-                                        p.q + (qrow0 + ri) * kRow)[8 * (4 * hf + c + jj) + lu];
+                                if (ri < rows_here)
+                                    x[jj][i] = reinterpret_cast<const uint4*>(qb + ri * kRow)[16 * cq + 4 * (c + jj) + lu];
                             }
-                        if (c == 0) {
-                            if (hf == 0) put_scale(scale_bits(e0, s.t0));
-                            // the transpose tiles double as staging buffer 1: before the first write to them, wait
-                            // until the sender has seen every copy of earlier messages read out
-                            bar_sync(kNbQFree, kSyncThreads);
-                        }
+                        // the transpose tiles are the staging buffers: before the first write to them, wait until the
+                        // sender has seen every copy of earlier messages read out (and, with it, the other warps)
+                        if (c == 0 && kseg > 0) ok = mbar_wait(&bars[kSBarQFree], (kseg - 1) & 1u, abort_flag, kLimitNs);
 #pragma unroll
                         for (int jj = 0; jj < 2; ++jj) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int ri = 4 * i + lr;
-                                *reinterpret_cast<uint4*>(qt + ri * 128 + ((lu ^ (ri & 7)) << 4)) = x[jj][i];
+                            for (int i = 0; i < 4; ++i) {
+                                const int ri = 8 * i + lr;
+                                *reinterpret_cast<uint4*>(qt + ri * 64 + ((lu ^ ((ri >> 1) & 3)) << 4)) = x[jj][i];
                             }
                             __syncwarp();
                             uint32_t v[32];
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const uint4 z = *reinterpret_cast<const uint4*>(qt + lane * 128 + ((u ^ (lane & 7)) << 4));
+                            for (int u = 0; u < 4; ++u) {
+                                const uint4 z = *reinterpret_cast<const uint4*>(qt + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4));
                                 v[4 * u] = z.x; v[4 * u + 1] = z.y; v[4 * u + 2] = z.z; v[4 * u + 3] = z.w;
                                 m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, z.x), z.y), z.z), z.w);
                             }
                             __syncwarp();
-                            tmem_st32(raw + 32 * (c + jj), v);
+                            tmem_st16(raw + 16 * (c + jj), v);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ri = 8 * i + (lane >> 2);
-                        *reinterpret_cast<uint4*>(qt + ri * 128 + (((lane & 3) ^ (ri & 7)) << 4)) = y[i];
+                    for (int i = 0; i < 2; ++i) {
+                        const int ri = 16 * i + (lane >> 1);
+                        *reinterpret_cast<uint4*>(qt + ri * 64 + (((lane & 1) ^ ((ri >> 1) & 3)) << 4)) = y[i];
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        y[u] = *reinterpret_cast<const uint4*>(qt + lane * 128 + ((u ^ (lane & 7)) << 4));
+                    for (int u = 0; u < 2; ++u) {
+                        y[u] = *reinterpret_cast<const uint4*>(qt + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4));
                         m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, y[u].x), y[u].y), y[u].z), y[u].w);
                     }
-                    // the row's largest magnitude, over both halves of its columns
-                    const uint32_t mine = max(m2 & 0xFFFFu, m2 >> 16);
-                    *xmine = __uint_as_float(mine);
-                    bar_sync(1 + qd, 64);
-                    const uint32_t top = max(mine, __float_as_uint(*xother));
+                    // the row's largest magnitude, over the four quarters of its columns
+                    ref_out[lane] = __uint_as_float(max(m2 & 0xFFFFu, m2 >> 16));
+                    mbar_arrive(&bars[kSBarQx + qd]);
+                    ok = mbar_wait(&bars[kSBarQx + qd], kseg & 1u, abort_flag, kLimitNs) && ok;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        top = max(top, reinterpret_cast<volatile uint32_t*>(smem + kSOffRef)[k * kRows + r]);
                     const int a = top < 0x7F80u ? row_exp(top) : 0;
                     const float inv = exp2_int(-a);
                     // an infinity or NaN in the query: every score of the row is NaN
                     rowf = top < 0x7F80u ? exp2_int(a) * p.scale_log2 : CUDART_NAN_F;
                     uint8_t* qr = smem + kSOffQR + r * 128;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    {
                         uint4 hi, lo;
-                        split4_q(y[2 * u].x, y[2 * u].y, inv, hi.x, lo.x);
-                        split4_q(y[2 * u].z, y[2 * u].w, inv, hi.y, lo.y);
-                        split4_q(y[2 * u + 1].x, y[2 * u + 1].y, inv, hi.z, lo.z);
-                        split4_q(y[2 * u + 1].z, y[2 * u + 1].w, inv, hi.w, lo.w);
-                        *reinterpret_cast<uint4*>(qr + (((2 * hf + u) ^ (r & 7)) << 4)) = hi;
-                        *reinterpret_cast<uint4*>(qr + (((4 + 2 * hf + u) ^ (r & 7)) << 4)) = lo;
+                        split4_q(y[0].x, y[0].y, inv, hi.x, lo.x);
+                        split4_q(y[0].z, y[0].w, inv, hi.y, lo.y);
+                        split4_q(y[1].x, y[1].y, inv, hi.z, lo.z);
+                        split4_q(y[1].z, y[1].w, inv, hi.w, lo.w);
+                        *reinterpret_cast<uint4*>(qr + ((cq ^ (r & 7)) << 4)) = hi;
+                        *reinterpret_cast<uint4*>(qr + (((4 + cq) ^ (r & 7)) << 4)) = lo;
                     }
+                    __syncwarp();
                     tmem_wait_st();
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t v[32], hi[32], lo[32];
                         tmem_ld32(raw + 32 * c, v);
                         tmem_wait_ld();
 #pragma unroll
                         for (int u = 0; u < 16; ++u) split4_q(v[2 * u], v[2 * u + 1], inv, hi[u], lo[u]);
-                        tmem_st16(t_lane + kColQ + 16 * (4 * hf + c), hi);
-                        tmem_st16(t_lane + kColQ + 128 + 16 * (4 * hf + c), lo);
+                        tmem_st16(t_lane + kColQ + 32 * cq + 16 * c, hi);
+                        tmem_st16(t_lane + kColQ + 128 + 32 * cq + 16 * c, lo);
                     }
                 }
                 fence_proxy_async_cta();
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars[kSBarQReady]);
-                uint32_t sc1 = scale_bits(e1, s.t0 + 1);
-                const int lim = row_ok ? (s.L - p.n_q + j + 1) : 0;  // keys 0 .. lim-1 are visible
-                RowRef ref;
-                ref.reset();
-                float l = 0.f;
+                // from here on a thread has rows rA = 32 qd + lane % 16 and rB = rA + 16, and 16 of the warp's columns: the
+                // tokens' scales are then read and unpacked once for two rows
+                const float rowfA = __shfl_sync(0xffffffffu, rowf, lane & 15), rowfB = __shfl_sync(0xffffffffu, rowf, 16 + (lane & 15));
+                const float2 fA = make_float2(rowfA, rowfA), fB = make_float2(rowfB, rowfB);
+                RowRef refA, refB;
+                refA.reset();
+                refB.reset();
+                float lA = 0.f, lB = 0.f;
+                const int limA = gA < p.R ? s.L - p.n_q + gA / p.H + 1 : 0;  // keys 0 .. lim-1 are visible
+                const int limB = gB < p.R ? s.L - p.n_q + gB / p.H + 1 : 0;
                 for (int t = s.t0; t < s.t1; ++t, ++n) {
                     const uint32_t sb = n & 1u, us = n >> 1;
+                    const uint32_t msg = 2 * n + (cq >> 1), stg = msg % kStages;
                     if (t == t_pf && have_next && row_ok)
-                        for (int c = hf; c < 9; c += 2) prefetch_l2(nq + 128 * c);
-                    bool ok = mbar_wait(&bars[kSBarSFull + sb], us & 1u, abort_flag, kLimitNs);
+                        for (int c = cq; c < 9; c += 4) prefetch_l2(nq + 128 * c);
+                    const uint4* sw4 = reinterpret_cast<const uint4*>(smem + kSOffScale + (n % kScaleBufs) * kScaleBytes) + cb / 8;
+                    ok = mbar_wait(&bars[kSBarSFull + sb], us & 1u, abort_flag, kLimitNs) && ok;
                     __syncwarp();
                     tc_fence_after();
-                    float y[64];
+                    float yA[16], yB[16];
                     {
-                        uint32_t a[32], b[32];
-                        tmem_ld32(t_lane + col_s(sb) + 64 * hf, a);
-                        tmem_ld32(t_lane + col_s(sb) + 64 * hf + 32, b);
+                        uint32_t a[16], b[16];
+                        tmem_ld16_halves(t_lane + col_s(sb) + 32 * cq, a);
+                        tmem_ld16_halves(t_lane + (16u << 16) + col_s(sb) + 32 * cq, b);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            y[k] = __uint_as_float(a[k]);
-                            y[32 + k] = __uint_as_float(b[k]);
+                        for (int k = 0; k < 16; ++k) {
+                            yA[k] = __uint_as_float(a[k]);
+                            yB[k] = __uint_as_float(b[k]);
                         }
                     }
                     tc_fence_before();
                     mbar_arrive(&bars[kSBarSEmpty + sb]);
                     // y = log2(p s_t), before the reference: S s_t (2^a scale log2 e) + log2 s_t
-                    const float4* sc4 = reinterpret_cast<const float4*>(smem + kSOffScale) + 16 * hf;
-                    const float4* ex4 = reinterpret_cast<const float4*>(smem + kSOffExp) + 16 * hf;
-                    const float4* in4 = reinterpret_cast<const float4*>(smem + kSOffInv) + 16 * hf;
-                    const float2 rowf2 = make_float2(rowf, rowf);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float4 sv = sc4[k], ev = ex4[k];
-                        const float2 y0 = fma2(mul2(make_float2(y[4 * k], y[4 * k + 1]), make_float2(sv.x, sv.y)), rowf2,
-                                               make_float2(ev.x, ev.y));
-                        const float2 y1 = fma2(mul2(make_float2(y[4 * k + 2], y[4 * k + 3]), make_float2(sv.z, sv.w)),
-                                               rowf2, make_float2(ev.z, ev.w));
-                        y[4 * k] = y0.x;
-                        y[4 * k + 1] = y0.y;
-                        y[4 * k + 2] = y1.x;
-                        y[4 * k + 3] = y1.y;
-                    }
-                    const int nvalid = lim - t * kTile - 64 * hf;  // columns < nvalid are visible
-                    if (nvalid < 64) {
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 sw = sw4[k], ew = sw4[k + kTile / 8];
+                        const uint32_t ss[4] = {sw.x, sw.y, sw.z, sw.w}, ee[4] = {ew.x, ew.y, ew.z, ew.w};
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) y[k] = k < nvalid ? y[k] : -CUDART_INF_F;
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = 8 * k + 2 * i;
+                            const float2 s2 = bf16x2_f32(ss[i]), e2f = bf16x2_f32(ee[i]);
+                            const float2 a2 = fma2(mul2(make_float2(yA[c], yA[c + 1]), s2), fA, e2f);
+                            const float2 b2 = fma2(mul2(make_float2(yB[c], yB[c + 1]), s2), fB, e2f);
+                            yA[c] = a2.x;
+                            yA[c + 1] = a2.y;
+                            yB[c] = b2.x;
+                            yB[c + 1] = b2.y;
+                        }
                     }
-                    const float half_top = fmax64(y);
-                    *xmine = half_top;
-                    bar_sync(1 + qd, 64);
-                    const int d = ref.move(fmaxf(half_top, *xother));
-                    const float2 mneg = make_float2(ref.minus(), ref.minus());
-                    float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
-                    uint32_t hi[16], lo[16];
+                    const int vA = limA - t * kTile - cb, vB = limB - t * kTile - cb;  // columns < v are visible
+                    if (vA < 16 || vB < 16) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float4 iv = in4[k];
-                        float2 p0 = add2(make_float2(y[4 * k], y[4 * k + 1]), mneg);
-                        float2 p1 = add2(make_float2(y[4 * k + 2], y[4 * k + 3]), mneg);
-                        p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
-                        p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
-                        ls0 = fma2(p0, make_float2(iv.x, iv.y), ls0);
-                        ls1 = fma2(p1, make_float2(iv.z, iv.w), ls1);
-                        split4_p(p0.x, p0.y, p1.x, p1.y, dither_pair(2 * k), dither_pair(2 * k + 1), hi[k], lo[k]);
+                        for (int k = 0; k < 16; ++k) {
+                            yA[k] = k < vA ? yA[k] : -CUDART_INF_F;
+                            yB[k] = k < vB ? yB[k] : -CUDART_INF_F;
+                        }
                     }
-                    const float lsum = (ls0.x + ls0.y) + (ls1.x + ls1.y);
-                    l = fmaf(l, RowRef::factor(d), lsum);
-                    if (bar_red_or(kNbFail, kSyncThreads, !ok || *abort_flag != 0)) {
-                        failed = true;
+                    float mA = fmax16(yA), mB = fmax16(yB);
+                    mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 16));
+                    mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 16));
+                    // the reference: the previous unit's (another warp's), moved if this unit needs it, handed on
+                    const float lastA = refA.R, lastB = refB.R;
+                    if (cq > 0 || t > s.t0) {
+                        ok = mbar_wait(bar_in, nref & 1u, abort_flag, kLimitNs) && ok;
+                        ++nref;
+                        refA.R = ref_in[lane & 15];
+                        refB.R = ref_in[16 + (lane & 15)];
+                    }
+                    const int dA = refA.move(mA), dB = refB.move(mB);
+                    if (cq < 3 || t + 1 < s.t1) {
+                        ref_out[lane] = lane < 16 ? refA.R : refB.R;
+                        mbar_arrive(bar_out);
+                    }
+                    const float2 nA = make_float2(refA.minus(), refA.minus()), nB = make_float2(refB.minus(), refB.minus());
+                    float2 sA = make_float2(0.f, 0.f), sB = sA;
+                    uint32_t hiA[4], loA[4], hiB[4], loB[4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 sw = sw4[k];
+                        const uint32_t ss[4] = {sw.x, sw.y, sw.z, sw.w};
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const int c = 8 * k + 2 * i, o = c / 4;
+                            const float2 i0 = bf16x2_f32(0x7F007F00u - ss[i]), i1 = bf16x2_f32(0x7F007F00u - ss[i + 1]);  // 1 / s
+                            float2 a0 = add2(make_float2(yA[c], yA[c + 1]), nA), a1 = add2(make_float2(yA[c + 2], yA[c + 3]), nA);
+                            a0 = make_float2(ex2_approx(a0.x), ex2_approx(a0.y));
+                            a1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
+                            sA = fma2(a0, i0, sA);
+                            sA = fma2(a1, i1, sA);
+                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
+                            float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
+                            b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
+                            b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
+                            sB = fma2(b0, i0, sB);
+                            sB = fma2(b1, i1, sB);
+                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
+                        }
+                    }
+                    // the sum is relative to the reference of this warp's last unit
+                    lA = fmaf(lA, RowRef::step(lastA, refA.R), sA.x + sA.y);
+                    lB = fmaf(lB, RowRef::step(lastB, refB.R), sB.x + sB.y);
+                    ok = mbar_wait(&bars[kSBarFree + stg], ((msg / kStages) & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
+                    // a row's 16 columns: the 16-byte unit (cb / 16) % 4 of its hi part and of its lo part
+                    uint8_t* stage = smem + kSOffStage + stg * kMsgStride;
+                    uint8_t* at = stage + (32 * qd + (lane & 15)) * 128;
+                    uint8_t* ah = at + ((((cb >> 4) & 3) ^ (lane & 7)) << 4);
+                    uint8_t* al = at + (((4 + ((cb >> 4) & 3)) ^ (lane & 7)) << 4);
+                    *reinterpret_cast<uint4*>(ah) = make_uint4(hiA[0], hiA[1], hiA[2], hiA[3]);
+                    *reinterpret_cast<uint4*>(ah + 2048) = make_uint4(hiB[0], hiB[1], hiB[2], hiB[3]);
+                    *reinterpret_cast<uint4*>(al) = make_uint4(loA[0], loA[1], loA[2], loA[3]);
+                    *reinterpret_cast<uint4*>(al + 2048) = make_uint4(loB[0], loB[1], loB[2], loB[3]);
+                    reinterpret_cast<int8_t*>(stage + kPBytes)[(cq & 1) * kRows + r] = static_cast<int8_t>(lane < 16 ? dA : dB);
+                    fence_proxy_async_cta();
+                    mbar_arrive(&bars[kSBarStaged + stg]);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
                         break;
                     }
-                    // every reader of this tile's scales is past them
-                    if (hf == 0) put_scale(sc1);
-                    sc1 = scale_bits(e2, t + 2);
-                    e2 = entry(t + 3);
-                    // the sender has seen the copy that last used this staging buffer (tile n - 2) read it
-                    bar_sync(kNbStageFree, kSyncThreads);
-                    uint8_t* stage = smem + ((n & 1u) ? kSOffStage1 : kSOffStage0);
-                    // row r, columns 64 hf ..: 16-byte units 4 hf + u at ((4 hf + u) ^ (r % 8)) of the hi and lo chunks
+                }
+                if (!ok) break;
+                // segment result: (R, l), l summed over the row's eight column parts; a NaN sum keeps its piece
+                lA += __shfl_xor_sync(0xffffffffu, lA, 16);
+                lB += __shfl_xor_sync(0xffffffffu, lB, 16);
+                float lt = lane < 16 ? lA : lB;
+                const float rmine = lane < 16 ? refA.R : refB.R;
+                if (cq < 3) {
+                    lx[2 * cq * kRows] = lt;
+                    lx[(2 * cq + 1) * kRows] = rmine;
+                    mbar_arrive(&bars[kSBarLx + qd]);
+                } else {
+                    ok = mbar_wait(&bars[kSBarLx + qd], kseg & 1u, abort_flag, kLimitNs);
+                    ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint8_t* at = stage + r * 128 + (((4 * hf + u) ^ (r & 7)) << 4);
-                        *reinterpret_cast<uint4*>(at) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-                        *reinterpret_cast<uint4*>(at + kRows * kTile) =
-                            make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-                    }
-                    if (hf == 0) reinterpret_cast<int8_t*>(stage + kPBytes)[r] = static_cast<int8_t>(d);
-                    fence_proxy_async_cta();
-                    bar_arrive(kNbStaged, kSyncThreads);
+                    for (int k = 0; k < 3; ++k)
+                        lt = fmaf(lx[2 * k * kRows], RowRef::step(lx[(2 * k + 1) * kRows], rmine), lt);
+                    if (row_ok && ok)
+                        p.ml_part[out_row_base + static_cast<int64_t>(s.slot) * kRows + r] =
+                            make_float2(lt != lt ? 0.f : rmine, lt);
                 }
-                if (failed) break;
-                // segment result: (R, l) with l summed over both column halves; a NaN sum keeps its piece
-                if (hf == 1) *xmine = l;
-                bar_sync(1 + qd, 64);
-                if (hf == 0 && row_ok) {
-                    const float lt = l + *xother;
-                    p.ml_part[out_row_base + static_cast<int64_t>(s.slot) * kRows + r] =
-                        make_float2(lt != lt ? 0.f : ref.R, lt);
-                }
-                bar_sync(1 + qd, 64);
+                ++kseg;
                 w = wn;
                 s = sn;
                 have = have_next;
             }
-            if (failed && tid == 0) raise_abort(abort_flag, peer_abort, p.dev_status);
-        } else if (warp == kWarpSender) {
-            // ---- sender: ships each staged P tile (one bulk copy, completing on the O CTA's barrier) once the O CTA
-            //      has released that message slot.  Takes the same per-tile barrier steps as the softmax warps.
-            const uint32_t peer_msg = mapa(sbase + kOOffMsg, peer);
-            const uint32_t peer_pfull = mapa(sbase + kOOffBar + kOBarPFull * 8, peer);
+            if (!ok) raise_abort(abort_flag, peer_abort, p.dev_status);
+        } else if (warp == kWarpScale) {
+            // ---- scales: the 128 tokens' s = 2^k and k of each tile, two tiles ahead of the softmax.  The buffer of tile n
+            //      was tile n - 4's; a softmax warp that has read the scores of tile n - 2 is past tile n - 3.
             SegWalk w = walk;
             Seg s;
             uint32_t n = 0;
-            bool failed = false;
-            while (!failed && w.next(p, s)) {
-                // every staged message read out before the Q reload reuses staging buffer 1
-                if (lane == 0) bulk_wait_group_read<0>();
-                __syncwarp();
-                bar_arrive(kNbQFree, kSyncThreads);
-                for (int t = s.t0; t < s.t1; ++t, ++n) {
-                    const uint32_t pb = n % kPSlots, up = n / kPSlots;
-                    if (bar_red_or(kNbFail, kSyncThreads, *abort_flag != 0)) {
-                        failed = true;
-                        break;
-                    }
-                    if (lane == 0) bulk_wait_group_read<1>();
+            bool ok = true;
+            while (ok && w.next(p, s)) {
+                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                    const uint32_t* src =
+                        reinterpret_cast<const uint32_t*>(block_of(p, s.tab[t], false) + kBlock8Scales) + 4 * lane;
+                    uint32_t bits[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) bits[i] = t * kTile + 4 * lane + i < s.L ? src[i] : 0x3F800000u;
+                    const uint32_t sb = n & 1u, us = n >> 1;
+                    ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
+                    uint2 sc, ex;
+                    uint32_t e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        e[i] = __float_as_uint(static_cast<float>(static_cast<int>(bits[i] >> 23) - 127));
+                    sc.x = __byte_perm(bits[0], bits[1], 0x7632);
+                    sc.y = __byte_perm(bits[2], bits[3], 0x7632);
+                    ex.x = __byte_perm(e[0], e[1], 0x7632);
+                    ex.y = __byte_perm(e[2], e[3], 0x7632);
+                    uint8_t* to = smem + kSOffScale + (n % kScaleBufs) * kScaleBytes + 8 * lane;
+                    *reinterpret_cast<uint2*>(to) = sc;
+                    *reinterpret_cast<uint2*>(to + 2 * kTile) = ex;
+                    ok = __all_sync(0xffffffffu, ok);
                     __syncwarp();
-                    bar_arrive(kNbStageFree, kSyncThreads);
-                    bar_sync(kNbStaged, kSyncThreads);
-                    if (lane == 0) {
-                        if (mbar_wait<true>(&bars[kSBarPEmpty + pb], (up & 1u) ^ 1u, abort_flag, kLimitNs)) {
-                            mbar_arrive_expect_tx_remote(peer_pfull + 8 * pb, kMsgBytes);
-                            bulk_copy_to_peer(peer_msg + pb * kMsgStride,
-                                              sbase + ((n & 1u) ? kSOffStage1 : kSOffStage0), kMsgBytes,
-                                              peer_pfull + 8 * pb);
-                            bulk_commit_group();
-                        } else {
-                            raise_abort(abort_flag, peer_abort, p.dev_status);
-                        }
-                    }
-                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kSBarSFull + sb]);
                 }
             }
+            if (!ok && lane == 0) raise_abort(abort_flag, peer_abort, p.dev_status);
+        } else if (warp == kWarpSender) {
+            // ---- sender: ships each staged P message (one bulk copy, completing on the O CTA's barrier) once the O CTA
+            //      has released that message slot
+            const uint32_t peer_msg = mapa(sbase + kOOffMsg, peer);
+            const uint32_t peer_pfull = mapa(sbase + kOOffBar + kOBarPFull * 8, peer);
             if (lane == 0) {
-                bulk_wait_group_read<0>();
+                SegWalk w = walk;
+                Seg s;
+                uint32_t u = 0;  // units
+                bool ok = true;
+                while (ok && w.next(p, s)) {
+                    const uint32_t first_u = u;
+                    for (int t = 2 * s.t0; t < 2 * s.t1; ++t, ++u) {
+                        const uint32_t stg = u % kStages, pb = u % kPSlots;
+                        ok = mbar_wait(&bars[kSBarStaged + stg], (u / kStages) & 1u, abort_flag, kLimitNs) &&
+                             mbar_wait<true>(&bars[kSBarPEmpty + pb], ((u / kPSlots) & 1u) ^ 1u, abort_flag, kLimitNs);
+                        if (!ok) break;
+                        bulk_copy_to_peer(peer_msg + pb * kMsgStride, sbase + kSOffStage + stg * kMsgStride, kMsgBytes,
+                                          peer_pfull + 8 * pb);
+                        bulk_commit_group();
+                        if (u > first_u) {
+                            bulk_wait_group_read<1>();  // the copy before this one has read its source
+                            mbar_arrive(&bars[kSBarFree + (u - 1) % kStages]);
+                        }
+                    }
+                    // every staged message read out before the Q reload reuses the staging buffers
+                    bulk_wait_group_read<0>();
+                    if (ok) {
+                        mbar_arrive(&bars[kSBarFree + (u - 1) % kStages]);
+                        mbar_arrive(&bars[kSBarQFree]);
+                    }
+                }
+                if (!ok) raise_abort(abort_flag, peer_abort, p.dev_status);
                 // the O CTA's last releases of its message slots arrive here: they have to land before this CTA ends
-                for (uint32_t i = (n > kPSlots ? n - kPSlots : 0); !failed && i < n; ++i)
+                for (uint32_t i = (u > kPSlots ? u - kPSlots : 0); ok && i < u; ++i)
                     mbar_wait<true>(&bars[kSBarPEmpty + i % kPSlots], (i / kPSlots) & 1u, abort_flag, kLimitNs);
             }
             __syncwarp();
@@ -569,24 +632,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             if (lane == 0) {
                 SegWalk w = walk;
                 Seg s;
-                uint32_t nv = 0;  // stage loads issued
+                uint32_t n = 0;  // tiles
                 bool ok = true;
                 const uint64_t last_use = l2_policy_evict_first();
                 while (ok && w.next(p, s)) {
-                    for (int t = s.t0; ok && t < s.t1; ++t) {
+                    for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                         const uint8_t* src = block_of(p, s.tab[t], true);
-                        for (int k = 0; k < 2; ++k, ++nv) {
-                            const uint32_t st = nv % kVStages, u = nv / kVStages;
-                            ok = mbar_wait(&bars[kOBarVEmpty + st], (u & 1u) ^ 1u, abort_flag, kLimitNs);
-                            if (!ok) break;
-                            mbar_arrive_expect_tx(&bars[kOBarVFull + st], kVStageBytes);
-                            bulk_load_hint(sbase + kOOffV + st * kVStageBytes, src + k * kVStageBytes, kVStageBytes,
-                                           &bars[kOBarVFull + st], last_use);
-                        }
+                        const uint32_t st = n % kVStages, u = n / kVStages;
+                        ok = mbar_wait(&bars[kOBarVEmpty + st], (u & 1u) ^ 1u, abort_flag, kLimitNs);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&bars[kOBarVFull + st], kVBytes);
+                        for (int k = 0; k < 2; ++k)
+                            bulk_load_hint(sbase + kOOffV + st * kVBytes + k * (kVBytes / 2), src + k * (kVBytes / 2),
+                                           kVBytes / 2, &bars[kOBarVFull + st], last_use);
                     }
                 }
                 if (!ok) raise_abort(abort_flag, peer_abort, p.dev_status);
-                for (uint32_t i = (nv > kVStages ? nv - kVStages : 0); i < nv; ++i)
+                for (uint32_t i = (n > kVStages ? n - kVStages : 0); i < n; ++i)
                     mbar_wait(&bars[kOBarVFull + i % kVStages], (i / kVStages) & 1u, &never, kLimitNs);
             }
         } else if (warp == kWarpMma) {
@@ -600,69 +662,72 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             const bool leader = elect_one();
             SegWalk w = walk;
             Seg s;
-            uint32_t n = 0, nv = 0, kseg = 0, nresc = 0;
+            uint32_t n = 0, kseg = 0, nresc = 0;
             bool ok = true;
             while (ok && w.next(p, s)) {
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
-                    const uint32_t pb = n % kPSlots, up = n / kPSlots;
-                    const bool fresh = (t == s.t0);
-                    if (leader) {
-                        ok = mbar_wait<true>(&bars[kOBarPFull + pb], up & 1u, abort_flag, kLimitNs);
-                        if (ok && fresh) ok = mbar_wait(&bars[kOBarOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs);
-                    }
-                    ok = __any_sync(0xffffffffu, ok && leader);
-                    if (!ok) break;
-                    const uint8_t* msg = smem + kOOffMsg + pb * kMsgStride;
-                    const bool resc = __any_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(msg + kPBytes)[lane] != 0);
-                    if (!fresh && resc) {
-                        // some row's reference moved: have the epilogue rescale O once all earlier MMAs are done
-                        if (leader) {
-                            *resc_pb = static_cast<int>(pb);
-                            mma_commit(smem_u32(&bars[kOBarODrain]));
-                            mbar_arrive(&bars[kOBarRescReq]);
-                            ok = mbar_wait(&bars[kOBarRescDone], nresc & 1u, abort_flag, kLimitNs);
-                        }
-                        ++nresc;
-                        ok = __any_sync(0xffffffffu, ok && leader);
-                        if (!ok) break;
-                    }
+                    const uint32_t st = n % kVStages;
                     const int nvalid = min(kTile, s.L - t * kTile);
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k, ++nv) {
-                        const uint32_t st = nv % kVStages, u = nv / kVStages;
-                        if (leader) ok = mbar_wait(&bars[kOBarVFull + st], u & 1u, abort_flag, kLimitNs);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u = 2 * n + h, pb = u % kPSlots;
+                        if (leader) {
+                            ok = mbar_wait<true>(&bars[kOBarPFull + pb], (u / kPSlots) & 1u, abort_flag, kLimitNs);
+                            if (ok) mbar_arrive_expect_tx(&bars[kOBarPFull + pb], kMsgBytes);  // for its next message
+                            if (ok && t == s.t0 && h == 0)
+                                ok = mbar_wait(&bars[kOBarOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs);
+                            if (ok && h == 0) ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
+                        }
                         ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
-                        uint8_t* vst = smem + kOOffV + st * kVStageBytes;
-                        if (nvalid < kTile) {
+                        if (h == 0 && nvalid < kTile) {
                             // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN)
                             const int nz = (kTile - nvalid) * 8;  // 16-byte units per chunk
-                            for (int i = lane; i < 2 * nz; i += 32) {
+                            for (int i = lane; i < 4 * nz; i += 32) {
                                 const int c = i / nz, q = i % nz;
-                                *reinterpret_cast<uint4*>(vst + c * kChunk + nvalid * 128 + q * 16) =
+                                *reinterpret_cast<uint4*>(smem + kOOffV + st * kVBytes + c * kChunk + nvalid * 128 + q * 16) =
                                     make_uint4(0, 0, 0, 0);
                             }
                             fence_proxy_async_cta();
                         }
-                        __syncwarp();
-                        if (leader) {
-                            tc_fence_after();
-                            const uint64_t vd = v_desc + (static_cast<uint64_t>(st * kVStageBytes) >> 4);
-                            const uint64_t pd = p_desc + (static_cast<uint64_t>(pb * kMsgStride) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                mma8_ss(tmem + 256 * k, pd + 2 * kk, vd + ((kk * 4096) >> 4), idesc_hi,
-                                        (fresh && kk == 0) ? 0u : 1u);
-                                mma8_ss(tmem + 256 * k, pd + ((kRows * kTile) >> 4) + 2 * kk, vd + ((kk * 4096) >> 4),
-                                        idesc_lo, 1u);
+                        // (read by every lane: which of the two units move some row's reference)
+                        const uint32_t* moved = reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes);
+                        const bool resc0 = __any_sync(0xffffffffu, moved[lane] != 0);
+                        const bool resc1 = __any_sync(0xffffffffu, moved[32 + lane] != 0);
+#pragma unroll 1
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const bool fresh = (t == s.t0 && h == 0 && kk == 0);
+                            if (!fresh && (kk ? resc1 : resc0)) {
+                                // have the epilogue rescale O once all earlier MMAs are done
+                                if (leader) {
+                                    *resc_pb = static_cast<int>(pb * kMsgStride + kk * kRows);
+                                    mma_commit(smem_u32(&bars[kOBarODrain]));
+                                    mbar_arrive(&bars[kOBarRescReq]);
+                                    ok = mbar_wait(&bars[kOBarRescDone], nresc & 1u, abort_flag, kLimitNs);
+                                }
+                                ++nresc;
+                                ok = __any_sync(0xffffffffu, ok && leader);
+                                if (!ok) break;
                             }
-                            mma_commit(smem_u32(&bars[kOBarVEmpty + st]));
+                            if (leader) {
+                                tc_fence_after();
+                                const uint64_t v = v_desc + (static_cast<uint64_t>(st * kVBytes + (2 * h + kk) * (kUnit * 128)) >> 4);
+                                const uint64_t pd = p_desc + (static_cast<uint64_t>(pb * kMsgStride + kk * 32) >> 4);
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    mma8_ss(tmem + 256 * k, pd, v + ((k * 2 * kChunk) >> 4), idesc_hi, fresh ? 0u : 1u);
+                                    mma8_ss(tmem + 256 * k, pd + 4, v + ((k * 2 * kChunk) >> 4), idesc_lo, 1u);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        if (leader) {
+                            mma_commit(peer_pempty + 8 * pb);
+                            if (h == 1) mma_commit(smem_u32(&bars[kOBarVEmpty + st]));
                         }
                         __syncwarp();
                     }
                     if (!ok) break;
-                    if (leader) mma_commit(peer_pempty + 8 * pb);
-                    __syncwarp();
                 }
                 if (!ok) break;
                 if (leader) mma_commit(smem_u32(&bars[kOBarOFull]));
@@ -675,10 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 mbar_wait(&bars[kOBarFin], 0, &never, kLimitNs);
             }
             __syncwarp();
-        } else if (warp < 4) {
-            // ---- epilogue: warps 0..3, one thread per query row
-            const int r = tid;
-            const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        } else if (warp < kSoftWarps) {
+            // ---- epilogue: warp (qd, cq), one thread per query row and 128 columns
+            const int r = 32 * (warp & 3) + lane, cq = warp >> 2;
+            const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * cq;
             SegWalk w = walk;
             Seg s;
             uint32_t kseg = 0, nresc = 0;
@@ -711,11 +776,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         __syncwarp();
                         tc_fence_after();
                         const int d =
-                            reinterpret_cast<const int8_t*>(smem + kOOffMsg + *resc_pb * kMsgStride + kPBytes)[r];
+                            reinterpret_cast<const int8_t*>(smem + kOOffMsg + kPBytes + *resc_pb)[r];
                         if (__any_sync(0xffffffffu, d != 0)) {
                             const float a = RowRef::factor(d);
 #pragma unroll 1
-                            for (int c = 0; c < 16; ++c) {
+                            for (int c = 0; c < 4; ++c) {
                                 uint32_t v[32];
                                 tmem_ld32(t_lane + 32 * c, v);
                                 tmem_wait_ld();
@@ -744,13 +809,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 float4* oseg = reinterpret_cast<float4*>(p.o_part) +
                                (out_row_base + static_cast<int64_t>(s.slot) * kRows) * (kDc / 4);
 #pragma unroll 1
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t v[32];
                     tmem_ld32(t_lane + 32 * c, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        oseg[(8 * c + k) * kRows + r] =
+                        oseg[(32 * cq + 8 * c + k) * kRows + r] =
                             make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
                                         __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
                 }
