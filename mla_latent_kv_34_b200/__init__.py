@@ -10,7 +10,6 @@ loudly if the shared library has not been built
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -96,21 +95,64 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
-def _on(stream, **tensors):
-    """Context of a call whose tensors are all on one device: that device is the current one, and ``stream`` (a
-    torch stream; None: the device's current one) too, so that what the call allocates belongs to that stream."""
-    devs = {t.device for t in tensors.values() if t is not None and t.is_cuda}
-    if len(devs) > 1 or (stream is not None and devs and stream.device not in devs):
-        raise MLAError("tensors and stream must be on one device")
-    if not devs:
-        return contextlib.nullcontext()  # no CUDA tensor: the checks of the arguments say which
-    return torch.cuda.device(devs.pop()) if stream is None else torch.cuda.stream(stream)
+class _Call:
+    """The checks and the context of one call of the 8-bit cache's functions: its tensors are on one CUDA device, which
+    is the current one inside the call, and so is ``stream`` (a torch stream; None: the device's current one), so that
+    what the call allocates belongs to that stream.
 
+    Nothing is done where it is so already: at the sizes of a decode step the host's part of a call counts.
+    """
 
-def _rope_ptr(rope_tab):
-    if rope_tab.dim() != 2 or rope_tab.shape[1] != D_R:
-        raise MLAError(f"rope_table must be float32 [rope_len, {D_R}]")
-    return _ptr(rope_tab, torch.float32, None, "rope_table")
+    __slots__ = ("dev", "raw", "ctx")
+
+    def __init__(self, stream, first, name):
+        if not first.is_cuda:
+            raise MLAError(f"{name} must be a CUDA tensor")
+        self.dev = first.get_device()
+        self.ctx = None
+        if stream is not None:
+            if stream.device.index != self.dev:
+                raise MLAError("tensors and stream must be on one device")
+            self.raw = stream.cuda_stream
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            self.raw = torch._C._cuda_getCurrentRawStream(self.dev)
+            if self.dev != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(self.dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def ptr(self, t, dtype, shape, name):
+        if t is None:
+            return None
+        if not t.is_cuda:
+            raise MLAError(f"{name} must be a CUDA tensor")
+        if t.get_device() != self.dev:
+            raise MLAError("tensors and stream must be on one device")
+        if not t.is_contiguous():
+            raise MLAError(f"{name} must be contiguous")
+        if dtype is not None and t.dtype is not dtype:
+            raise MLAError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise MLAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        return t.data_ptr()
+
+    def pool(self, t, block_bytes, name):
+        if t.dim() != 2 or t.shape[1] != block_bytes:
+            raise MLAError(f"{name} must be uint8 [cap_blocks, {block_bytes}]")
+        return self.ptr(t, torch.uint8, None, name)
+
+    def table(self, t, B, name="block_table"):
+        if t.dim() != 2 or (B is not None and t.shape[0] != B):
+            raise MLAError(f"{name} must be int32 [B, max_blocks]")
+        return self.ptr(t, torch.int32, None, name)
 
 
 def rope_table(rope_len: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -219,36 +261,30 @@ def new_cache8(cap_blocks: int, device="cuda") -> torch.Tensor:
     return torch.empty((cap_blocks, BLOCK8_BYTES), dtype=torch.uint8, device=device)
 
 
-def _cache8_ptr(cache8):
-    if cache8.dim() != 2 or cache8.shape[1] != BLOCK8_BYTES:
-        raise MLAError(f"cache8 must be uint8 [cap_blocks, {BLOCK8_BYTES}]")
-    return _ptr(cache8, torch.uint8, None, "cache8")
-
-
 def append_cache8(cache8, block_table, seq_idx, pos, c_kv, k_rope, rope_tab, dev_status=None, stream=None):
     """Quantise the rows [c_kv [T,512] | R_pos k_rope [T,64]] to 576 e4m3 codes and a power-of-two scale each and
     write them at token pos of sequence seq_idx of an 8-bit cache."""
     T = c_kv.shape[0]
-    tp, mb = _table(block_table)
-    with _on(stream, cache8=cache8, block_table=block_table, seq_idx=seq_idx, pos=pos, c_kv=c_kv, k_rope=k_rope,
-             rope_tab=rope_tab, dev_status=dev_status):
+    if rope_tab.dim() != 2 or rope_tab.shape[1] != D_R:
+        raise MLAError(f"rope_table must be float32 [rope_len, {D_R}]")
+    with _Call(stream, cache8, "cache8") as c:
         _check(lib.mla_append_cache8(
-            _cache8_ptr(cache8), cache8.shape[0], tp, block_table.shape[0], mb,
-            _ptr(seq_idx, torch.int32, (T,), "seq_idx"), _ptr(pos, torch.int32, (T,), "pos"),
-            _ptr(c_kv, torch.bfloat16, (T, D_C), "c_kv"), _ptr(k_rope, torch.bfloat16, (T, D_R), "k_rope"),
-            _rope_ptr(rope_tab), rope_tab.shape[0], T, _ptr(dev_status, torch.int32, None, "dev_status"),
-            _stream(stream)))
+            c.pool(cache8, BLOCK8_BYTES, "cache8"), cache8.shape[0], c.table(block_table, None), block_table.shape[0],
+            block_table.shape[1], c.ptr(seq_idx, torch.int32, (T,), "seq_idx"), c.ptr(pos, torch.int32, (T,), "pos"),
+            c.ptr(c_kv, torch.bfloat16, (T, D_C), "c_kv"), c.ptr(k_rope, torch.bfloat16, (T, D_R), "k_rope"),
+            c.ptr(rope_tab, torch.float32, None, "rope_table"), rope_tab.shape[0], T,
+            c.ptr(dev_status, torch.int32, None, "dev_status"), c.raw))
 
 
 def read_cache8(cache8, block_table8, kv_len, cache, block_table, dev_status=None, stream=None):
     """Bring the first kv_len[b] tokens of every sequence of an 8-bit cache back into the bf16 pool ``cache``."""
     B = kv_len.shape[0]
-    with _on(stream, cache8=cache8, block_table8=block_table8, kv_len=kv_len, cache=cache, block_table=block_table,
-             dev_status=dev_status):
+    with _Call(stream, cache8, "cache8") as c:
         _check(lib.mla_read_cache8(
-            _cache8_ptr(cache8), cache8.shape[0], *_table(block_table8, B), _ptr(kv_len, torch.int32, (B,), "kv_len"),
-            B, _cache_ptr(cache), cache.shape[0], *_table(block_table, B),
-            _ptr(dev_status, torch.int32, None, "dev_status"), _stream(stream)))
+            c.pool(cache8, BLOCK8_BYTES, "cache8"), cache8.shape[0], c.table(block_table8, B, "block_table8"),
+            block_table8.shape[1], c.ptr(kv_len, torch.int32, (B,), "kv_len"), B, c.pool(cache, BLOCK_BYTES, "cache"),
+            cache.shape[0], c.table(block_table, B), block_table.shape[1],
+            c.ptr(dev_status, torch.int32, None, "dev_status"), c.raw))
     return cache
 
 
@@ -263,19 +299,18 @@ def decode8(q, cache8, block_table, kv_len, W_UV, n_q: int, scale: float, num_sp
     T, H = q.shape[0], q.shape[1]
     if T != B * n_q:
         raise MLAError("q rows must equal len(kv_len) * n_q")
-    with _on(stream, q=q, cache8=cache8, block_table=block_table, kv_len=kv_len, W_UV=W_UV, workspace=workspace, out=out,
-             lse_out=lse_out, dev_status=dev_status):
+    with _Call(stream, q, "q") as c:
         if workspace is None:
             workspace = torch.empty(decode8_workspace_bytes(B, n_q, H, num_splits), dtype=torch.uint8, device=q.device)
         if out is None:
             out = torch.empty((T, H, D_H), dtype=torch.bfloat16, device=q.device)
         _check(lib.mla_decode8(
-            _ptr(q, torch.bfloat16, (T, H, D_ROW), "q"), _cache8_ptr(cache8), cache8.shape[0], *_table(block_table, B),
-            _ptr(kv_len, torch.int32, (B,), "kv_len"),
-            _ptr(W_UV, torch.bfloat16, (H, D_H, D_C), "W_UV"), B, n_q, H, float(scale), num_splits,
-            _ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size(),
-            _ptr(out, torch.bfloat16, (T, H, D_H), "out"), _ptr(lse_out, torch.float32, (T, H), "lse_out"),
-            _ptr(dev_status, torch.int32, None, "dev_status"), _stream(stream)))
+            c.ptr(q, torch.bfloat16, (T, H, D_ROW), "q"), c.pool(cache8, BLOCK8_BYTES, "cache8"), cache8.shape[0],
+            c.table(block_table, B), block_table.shape[1], c.ptr(kv_len, torch.int32, (B,), "kv_len"),
+            c.ptr(W_UV, torch.bfloat16, (H, D_H, D_C), "W_UV"), B, n_q, H, scale, num_splits,
+            c.ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size(),
+            c.ptr(out, torch.bfloat16, (T, H, D_H), "out"), c.ptr(lse_out, torch.float32, (T, H), "lse_out"),
+            c.ptr(dev_status, torch.int32, None, "dev_status"), c.raw))
     return out
 
 
