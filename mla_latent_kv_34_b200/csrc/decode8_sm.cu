@@ -1,0 +1,645 @@
+// Absorbed MLA decode over the 8-bit cache for few query rows (few heads): one SM per work unit.
+//
+// The attend phase of mla_decode8, with both contractions transposed, the 128 tokens of a block as the M side:
+//   S^T[token, row] = K . [Q_hi | Q_lo]^T   M = 128 tokens (A: the block's codes as they lie), N = 2 NR: 18 MMAs
+//   O^T[latent, row] += V^T . [P_hi | P_lo]^T   M = 128 latent columns per block of four (A: the same codes, MN-major),
+//                                           K = 128 tokens in steps of 32: 16 MMAs of N = 2 NR (hi and lo in columns of
+//                                           their own, added at the end), or 32 of N = NR where that does not fit
+// (NR: the rows rounded up to 16, 32 or 48).  Scores and O^T fit one SM's tensor memory, so a block is read once, by one
+// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token, 1.67 us a block and SM with all SMs reading; the
+// MMAs of a block take about half of that, and a ring of two blocks keeps the reads going (the bf16 kernel's ring holds
+// one, and its reads wait for its MMAs).
+//
+// Softmax: a thread per token (tensor-memory lane) and half the rows.  The four warps of a set take 32 tokens each, a
+// unit; they hand the rows' reference exponents on (RowRef in decode8_common.cuh), so no barrier holds them in step.  A
+// row's maximum over a unit is a warp reduction; the token's scale is one register.
+//
+// Warps: 0..7 softmax (set = warp / 4), 8 copies, 9 MMAs, 12..15 rescaling of O^T and a segment's output.  Scheduling and
+// output are the pair kernel's (decode8_tc.cu).  Every wait is bounded.
+#include <cuda.h>
+#include <math_constants.h>
+
+#include "decode8_common.cuh"
+
+namespace mla {
+
+namespace sm8 {
+
+using namespace d8;
+
+constexpr int kChunk = kBlock8Chunk;
+constexpr int kSoftWarps = 8, kSoftThreads = 256;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpEpi = 12;
+constexpr int kThreads = 512;
+
+constexpr int kBFull = 0, kBEmpty = 4, kBSFull = 8, kBSEmpty = 10, kBPReady = 12, kBPFree = 14, kBRef = 16, kBQReady = 24,
+              kBOFull = 25, kBOFree = 26, kBRescReq = 27, kBRescDone = 28, kBODrain = 29, kBLReady = 30, kBFin = 31,
+              kNumBars = 32;
+
+template <int NR>
+struct Lay {
+    static constexpr bool kStack = 12 * NR <= 512;           // hi and lo of P in accumulator columns of their own
+    static constexpr int kN = 2 * NR;                        // columns of a score buffer
+    static constexpr int kOC = kStack ? 2 * NR : NR;         // accumulator columns of a latent block
+    static constexpr int kRN = NR / 2;                       // rows of a softmax thread
+    static constexpr uint32_t kTmemCols = 2 * kN + 4 * kOC <= 256 ? 256 : 512;
+    static constexpr int kOffRing = 0;                       // two tiles
+    static constexpr int kQChunk = kN * 128;                 // [hi rows | lo rows] x 128 columns, swizzled
+    static constexpr int kOffQ = 2 * kTileBytes;             // four chunks, then the RoPE columns (64 bytes a row)
+    static constexpr int kOffP = kOffQ + 4 * kQChunk + kN * 64;
+    static constexpr int kPBytes = kN * 128;                 // [hi rows | lo rows] x 128 tokens, swizzled
+    static constexpr int kOffD = kOffP + 2 * kPBytes;        // [2 buffers][4 units][NR] int8 rescale exponents
+    static constexpr int kOffRowF = kOffD + 8 * NR;          // [NR] fp32: 2^a scale log2 e
+    static constexpr int kOffRef = kOffRowF + 4 * NR;        // [8 warps][kRN] reference exponents
+    static constexpr int kOffFac = kOffRef + 8 * kRN * 4;    // [8 warps][kRN] factors of the sums
+    static constexpr int kOffL = kOffFac + 8 * kRN * 4;      // [8 warps][kRN] (sum, reference) of a segment
+    static constexpr int kOffBar = kOffL + 8 * kRN * 8;
+    static constexpr int kOffTail = kOffBar + kNumBars * 8;  // tmem base, abort flag, rescale place, [total, sequence, tile]
+    static constexpr int kSmemBytes = kOffTail + 32;
+    static_assert(2 * kN + 4 * kOC <= 512, "tensor memory");
+    static_assert(kOffQ % 1024 == 0 && kQChunk % 1024 == 0 && kOffP % 1024 == 0 && kPBytes % 1024 == 0, "swizzle atoms");
+    static_assert(kOffD % 16 == 0 && kOffRowF % 16 == 0 && kOffRef % 16 == 0 && kOffL % 16 == 0 && kOffBar % 8 == 0, "");
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    __device__ static constexpr uint32_t col_s(uint32_t sb) { return sb * kN; }
+    __device__ static constexpr uint32_t col_o(uint32_t c) { return 2 * kN + c * kOC; }
+};
+
+__device__ __forceinline__ void raise_abort(volatile int* abort_flag, int32_t* dev_status) {
+    *abort_flag = 1;
+    if (dev_status) atomicOr(dev_status, MLA_DEVERR_TIMEOUT);
+}
+
+// Maximum over the warp's 32 lanes (NaN only if all are).
+__device__ __forceinline__ float warp_max_f32(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// N columns of this warp's 32 lanes (N = 8, 16, 24 or 32).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+template <int NR>
+__global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p) {
+    using L = Lay<NR>;
+    constexpr int RN = L::kRN;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffTail);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffTail + 4);
+    volatile int* resc_at = reinterpret_cast<volatile int*>(smem + L::kOffTail + 8);
+    int* first = reinterpret_cast<int*>(smem + L::kOffTail + 12);
+    volatile int never = 0;
+
+    if ((sbase & 1023u) != 0) {
+        if (tid == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEVERR_TIMEOUT);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars[kBFull + i], 1);
+            mbar_init(&bars[kBEmpty + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[kBSFull + i], 1);
+            mbar_init(&bars[kBSEmpty + i], kSoftThreads);
+            mbar_init(&bars[kBPReady + i], kSoftThreads);
+            mbar_init(&bars[kBPFree + i], 1);
+        }
+        for (int i = 0; i < 8; ++i) mbar_init(&bars[kBRef + i], 1);
+        mbar_init(&bars[kBQReady], kSoftThreads);
+        mbar_init(&bars[kBOFull], 1);
+        mbar_init(&bars[kBOFree], 128);
+        mbar_init(&bars[kBRescReq], 1);
+        mbar_init(&bars[kBRescDone], 128);
+        mbar_init(&bars[kBODrain], 1);
+        mbar_init(&bars[kBLReady], kSoftWarps);
+        mbar_init(&bars[kBFin], 1);
+        *abort_flag = 0;
+        *resc_at = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpProducer) tmem_alloc(tmem_slot, L::kTmemCols);
+    // everything above touches only this CTA's own resources; the call's inputs are read after this wait
+    grid_dependency_wait();
+    const int pidx = static_cast<int>(blockIdx.x);
+    if (warp == 0) find_first(p, pidx, lane, first);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int Nt = first[0];
+    SegWalk walk;
+    walk.b = first[1];
+    walk.tb = first[2];
+    walk.lo = static_cast<int>((static_cast<int64_t>(pidx) * Nt) / p.P_g);
+    walk.hi = static_cast<int>((static_cast<int64_t>(pidx + 1) * Nt) / p.P_g);
+    walk.pidx = pidx;
+
+    if (warp == kWarpProducer) {
+        // ---- copies: a tile's codes as 32 and 40 KB, read by this SM only, once
+        if (lane == 0) {
+            SegWalk w = walk;
+            Seg s;
+            uint32_t n = 0;
+            bool ok = true;
+            const uint64_t once = l2_policy_evict_first();
+            while (ok && w.next(p, s)) {
+                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                    const uint8_t* src = block_of(p, s.tab[t], true);
+                    const uint32_t u = n >> 1, base = (n & 1u) * kTileBytes, bi = 2 * (n & 1u);
+                    ok = mbar_wait(&bars[kBEmpty + bi], (u & 1u) ^ 1u, abort_flag, kLimitNs);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars[kBFull + bi], kCopyA);
+                    bulk_load_hint(sbase + L::kOffRing + base, src, kCopyA, &bars[kBFull + bi], once);
+                    // (both halves of a slot are released together)
+                    ok = mbar_wait(&bars[kBEmpty + bi + 1], (u & 1u) ^ 1u, abort_flag, kLimitNs);
+                    if (!ok) {
+                        mbar_wait(&bars[kBFull + bi], u & 1u, &never, kLimitNs);
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bars[kBFull + bi + 1], kCopyB);
+                    bulk_load_hint(sbase + L::kOffRing + base + kCopyA, src + kCopyA, kCopyB, &bars[kBFull + bi + 1], once);
+                }
+            }
+            if (!ok) raise_abort(abort_flag, p.dev_status);
+            // let every issued copy land before the CTA can exit
+            for (uint32_t i = (n > 2 ? n - 2 : 0); i < n; ++i)
+                for (int k = 0; k < 2; ++k)
+                    mbar_wait(&bars[kBFull + 2 * (i & 1u) + k], (i >> 1) & 1u, &never, kLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ---- MMA issuer: the scores of a tile go out before the tile before it is aggregated
+        const bool leader = elect_one();
+        constexpr uint32_t idesc_s = idesc_f8_f32(128, L::kN, false, false);
+        constexpr uint32_t idesc_hi = idesc_f8_f32(128, NR, true, false);
+        constexpr uint32_t idesc_lo = idesc_f8_f32(128, NR, true, false, false, true);
+        const uint64_t k_desc = sdesc_sw128(sbase + L::kOffRing, 16, 1024);            // K-major chunks
+        const uint64_t kr_desc = sdesc_sw64(sbase + L::kOffRing + kBlock8Rope, 16, 512);
+        const uint64_t v_desc = sdesc_sw128(sbase + L::kOffRing, kChunk, 1024);        // the same chunks MN-major
+        const uint64_t q_desc = sdesc_sw128(sbase + L::kOffQ, 16, 1024);
+        const uint64_t qr_desc = sdesc_sw64(sbase + L::kOffQ + 4 * L::kQChunk, 16, 512);
+        const uint64_t p_desc = sdesc_sw128(sbase + L::kOffP, 16, 1024);
+        SegWalk w = walk;
+        Seg s;
+        uint32_t n = 0, kseg = 0, nresc = 0;
+        bool ok = true;
+        while (ok && w.next(p, s)) {
+            if (leader) ok = mbar_wait(&bars[kBQReady], kseg & 1u, abort_flag, kLimitNs);
+            ok = __any_sync(0xffffffffu, ok && leader);
+            // step t issues the scores of tile t and aggregates tile t - 1
+            for (int t = s.t0; ok && t <= s.t1; ++t, ++n) {
+                if (t < s.t1) {
+                    const uint32_t sb = n & 1u, us = n >> 1;
+                    const int nvalid = min(kTile, s.L - t * kTile);
+                    if (leader) {
+                        ok = mbar_wait(&bars[kBSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
+                        for (int k = 0; ok && k < 2; ++k)
+                            ok = mbar_wait(&bars[kBFull + 2 * sb + k], us & 1u, abort_flag, kLimitNs);
+                    }
+                    ok = __any_sync(0xffffffffu, ok && leader);
+                    if (!ok) break;
+                    if (nvalid < kTile) {
+                        // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN); their scores are masked
+                        const int nz = (kTile - nvalid) * 8;  // 16-byte units per chunk
+                        for (int i = lane; i < 4 * nz; i += 32) {
+                            const int c = i / nz, u = i % nz;
+                            *reinterpret_cast<uint4*>(smem + L::kOffRing + sb * kTileBytes + c * kChunk + nvalid * 128 + u * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_cta();
+                    }
+                    __syncwarp();
+                    if (leader) {
+                        tc_fence_after();
+                        const uint64_t off = static_cast<uint64_t>(sb * kTileBytes) >> 4;
+                        const uint32_t d = tmem + L::col_s(sb);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma8_ss(d, k_desc + off + ((c * kChunk + kk * 32) >> 4), q_desc + ((c * L::kQChunk + kk * 32) >> 4),
+                                        idesc_s, (c | kk) ? 1u : 0u);
+                        mma8_ss(d, kr_desc + off, qr_desc, idesc_s, 1u);
+                        mma8_ss(d, kr_desc + off + 2, qr_desc + 2, idesc_s, 1u);
+                        mma_commit(smem_u32(&bars[kBSFull + sb]));
+                    }
+                    __syncwarp();
+                }
+                if (t > s.t0) {
+                    const uint32_t m = n - 1, pb = m & 1u, um = m >> 1;
+                    const bool seg_first = (t - 1 == s.t0);
+                    if (leader) {
+                        ok = mbar_wait(&bars[kBPReady + pb], um & 1u, abort_flag, kLimitNs);
+                        if (ok && seg_first) ok = mbar_wait(&bars[kBOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs);
+                    }
+                    ok = __any_sync(0xffffffffu, ok && leader);
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int u = 0; u < 4; ++u) {
+                        const bool fresh = seg_first && u == 0;
+                        const uint8_t* moved = smem + L::kOffD + (4 * pb + u) * NR;
+                        const bool resc = __any_sync(0xffffffffu, 4 * lane < NR && reinterpret_cast<const uint32_t*>(moved)[lane] != 0);
+                        if (!fresh && resc) {
+                            // some row's reference moved: have O^T rescaled once all earlier MMAs are done
+                            if (leader) {
+                                *resc_at = static_cast<int>((4 * pb + u) * NR);
+                                mma_commit(smem_u32(&bars[kBODrain]));
+                                mbar_arrive(&bars[kBRescReq]);
+                                ok = mbar_wait(&bars[kBRescDone], nresc & 1u, abort_flag, kLimitNs);
+                            }
+                            ++nresc;
+                            ok = __any_sync(0xffffffffu, ok && leader);
+                            if (!ok) break;
+                        }
+                        if (leader) {
+                            tc_fence_after();
+                            const uint64_t v = v_desc + (static_cast<uint64_t>(pb * kTileBytes + u * 4096) >> 4);
+                            const uint64_t pd = p_desc + (static_cast<uint64_t>(pb * L::kPBytes + u * 32) >> 4);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t o = tmem + L::col_o(c);
+                                const uint64_t vc = v + ((c * kChunk) >> 4);
+                                mma8_ss(o, vc, pd, idesc_hi, fresh ? 0u : 1u);
+                                mma8_ss(L::kStack ? o + NR : o, vc, pd + ((NR * 128) >> 4), idesc_lo,
+                                        (L::kStack && fresh) ? 0u : 1u);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (leader) {
+                        mma_commit(smem_u32(&bars[kBEmpty + 2 * pb]));
+                        mma_commit(smem_u32(&bars[kBEmpty + 2 * pb + 1]));
+                        mma_commit(smem_u32(&bars[kBPFree + pb]));
+                    }
+                    __syncwarp();
+                }
+            }
+            --n;  // (the last step issued no scores)
+            if (!ok) break;
+            if (leader) mma_commit(smem_u32(&bars[kBOFull]));
+            __syncwarp();
+            ++kseg;
+        }
+        if (!ok && leader) raise_abort(abort_flag, p.dev_status);
+        if (leader) {
+            mma_commit(smem_u32(&bars[kBFin]));
+            mbar_wait(&bars[kBFin], 0, &never, kLimitNs);
+        }
+        __syncwarp();
+    } else if (warp < kSoftWarps) {
+        // ---- softmax: set k has rows k RN .. k RN + RN - 1; thread = token 32 qd + lane of a tile
+        const int qd = warp & 3, set = warp >> 2, row0 = set * RN;
+        const int tk = 32 * qd + lane;
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
+        volatile float* ref_in = reinterpret_cast<volatile float*>(smem + L::kOffRef) + (4 * set + ((qd + 3) & 3)) * RN;
+        float* ref_out = reinterpret_cast<float*>(smem + L::kOffRef) + warp * RN;
+        float* fac = reinterpret_cast<float*>(smem + L::kOffFac) + warp * RN;
+        uint64_t* bar_in = &bars[kBRef + 4 * set + ((qd + 3) & 3)];
+        uint64_t* bar_out = &bars[kBRef + warp];
+        const float* rowf_all = reinterpret_cast<const float*>(smem + L::kOffRowF);
+        // the token's dither (multiples of the golden ratio over the tokens), for both halves of a pair of rows
+        const uint32_t dither = (((static_cast<uint32_t>(tk) * 40503u + 20251u) >> 8) & 0xFFu) * 0x00010001u;
+        SegWalk w = walk;
+        Seg s;
+        uint32_t n = 0, kseg = 0, nref = 0;
+        bool ok = true;
+        while (ok && w.next(p, s)) {
+            // the token's scale in the tiles to come, a tile ahead (the table entry two ahead)
+            auto entry = [&](int t) { return t < s.t1 ? s.tab[t] : 0; };
+            auto scale_bits = [&](int32_t e, int t) {
+                return (t < s.t1 && t * kTile + tk < s.L)
+                           ? reinterpret_cast<const uint32_t*>(block_of(p, e, false) + kBlock8Scales)[tk]
+                           : 0x3F800000u;
+            };
+            const int32_t e0 = entry(s.t0);
+            int32_t e1 = entry(s.t0 + 1);
+            // the segment's query rows as hi and lo codes.  The previous segment's score MMAs are done (this warp has read
+            // its last scores), but other warps may still want the rows' factors: they are read before the last tile's
+            // P is announced.
+            {
+                constexpr int kRW = NR / kSoftWarps;  // rows a warp: warp, warp + 8, ..
+                uint4 x[kRW][3];
+#pragma unroll
+                for (int i = 0; i < kRW; ++i) {
+                    const int r = warp + kSoftWarps * i;
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s.b) * p.R + r) * kRow);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        x[i][k] = make_uint4(0, 0, 0, 0);
+                        if (r < p.R && lane + 32 * k < 72) x[i][k] = src[lane + 32 * k];
+                    }
+                }
+                if (kseg > 0)  // every warp past the last tile
+                    ok = mbar_wait(&bars[kBLReady], (kseg - 1) & 1u, abort_flag, kLimitNs);
+#pragma unroll
+                for (int i = 0; i < kRW; ++i) {
+                    const int r = warp + kSoftWarps * i;
+                    uint32_t m2 = 0;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[i][k].x), x[i][k].y), x[i][k].z), x[i][k].w);
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+                    const int a = top < 0x7F80u ? row_exp(top) : 0;
+                    const float inv = exp2_int(-a);
+                    // an infinity or NaN in the query: every score of the row is NaN
+                    if (lane == 0)
+                        reinterpret_cast<float*>(smem + L::kOffRowF)[r] = top < 0x7F80u ? exp2_int(a) * p.scale_log2 : CUDART_NAN_F;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const int u = lane + 32 * k;  // columns 8 u .. 8 u + 7
+                        if (u >= 72) continue;
+                        uint2 hi, lo;
+                        split4_q(x[i][k].x, x[i][k].y, inv, hi.x, lo.x);
+                        split4_q(x[i][k].z, x[i][k].w, inv, hi.y, lo.y);
+                        const int rl = NR + r;
+                        uint8_t *ah, *al;
+                        if (u < 64) {
+                            uint8_t* c = smem + L::kOffQ + (u >> 4) * L::kQChunk + (u & 1) * 8;
+                            ah = c + r * 128 + ((((u >> 1) & 7) ^ (r & 7)) << 4);
+                            al = c + rl * 128 + ((((u >> 1) & 7) ^ (rl & 7)) << 4);
+                        } else {
+                            uint8_t* c = smem + L::kOffQ + 4 * L::kQChunk + (u & 1) * 8;
+                            ah = c + r * 64 + ((((u >> 1) & 3) ^ ((r >> 1) & 3)) << 4);
+                            al = c + rl * 64 + ((((u >> 1) & 3) ^ ((rl >> 1) & 3)) << 4);
+                        }
+                        *reinterpret_cast<uint2*>(ah) = hi;
+                        *reinterpret_cast<uint2*>(al) = lo;
+                    }
+                }
+            }
+            fence_proxy_async_cta();
+            tc_fence_before();
+            mbar_arrive(&bars[kBQReady]);
+            ok = mbar_wait(&bars[kBQReady], kseg & 1u, abort_flag, kLimitNs) && ok;  // every row's factor is there
+            float rowf[RN], lp[RN];
+#pragma unroll
+            for (int i = 0; i < RN; ++i) {
+                rowf[i] = rowf_all[row0 + i];
+                lp[i] = 0.f;
+            }
+            uint32_t sc = scale_bits(e0, s.t0);
+            RowRef ref;  // lane i < RN: row row0 + i
+            ref.reset();
+            const int lim0 = s.L - p.n_q + 1;  // keys below this are visible to every query of the step
+            for (int t = s.t0; t < s.t1; ++t, ++n) {
+                const uint32_t sb = n & 1u, us = n >> 1;
+                const float st = __uint_as_float(sc), inv_s = __uint_as_float(0x7F000000u - sc);
+                const float et = static_cast<float>(static_cast<int>(sc >> 23) - 127);
+                sc = scale_bits(e1, t + 1);
+                e1 = entry(t + 2);
+                ok = mbar_wait(&bars[kBSFull + sb], us & 1u, abort_flag, kLimitNs) && ok;
+                __syncwarp();
+                tc_fence_after();
+                float y[RN];
+                {
+                    uint32_t h[RN], l[RN];
+#pragma unroll
+                    for (int i = 0; i < RN; i += 8) {
+                        tmem_ld8(t_lane + L::col_s(sb) + row0 + i, h + i);
+                        tmem_ld8(t_lane + L::col_s(sb) + NR + row0 + i, l + i);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < RN; ++i) y[i] = __uint_as_float(h[i]) + __uint_as_float(l[i]);
+                }
+                tc_fence_before();
+                mbar_arrive(&bars[kBSEmpty + sb]);
+                const int tok = t * kTile + tk;
+                // y = log2(p s_t), before the reference
+#pragma unroll
+                for (int i = 0; i < RN; ++i) y[i] = fmaf(y[i] * st, rowf[i], et);
+                if (tok >= lim0) {
+#pragma unroll
+                    for (int i = 0; i < RN; ++i)
+                        if (tok >= lim0 + (row0 + i) / p.H) y[i] = -CUDART_INF_F;
+                }
+                // the unit's row maxima: lane i gets row row0 + i's
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < RN; ++i) {
+                    const float v = warp_max_f32(y[i]);
+                    if (lane == i) top = v;
+                }
+                if (row0 + lane >= p.R) top = -CUDART_INF_F;  // rows of no query: P = 0 (y = -inf below)
+                // the references: the previous unit's (another warp's), moved where this unit needs it, handed on
+                const float last = ref.R;
+                if (qd > 0 || t > s.t0) {
+                    ok = mbar_wait(bar_in, nref & 1u, abort_flag, kLimitNs) && ok;
+                    ++nref;
+                    if (lane < RN) ref.R = ref_in[lane];
+                }
+                const int d = ref.move(top);
+                const float step = RowRef::step(last, ref.R);
+                if (lane < RN) {
+                    ref_out[lane] = ref.R;
+                    fac[lane] = step;
+                }
+                __syncwarp();
+                if (lane == 0 && (qd < 3 || t + 1 < s.t1)) mbar_arrive(bar_out);
+                if (__any_sync(0xffffffffu, lane < RN && step != 1.f)) {
+#pragma unroll
+                    for (int i = 0; i < RN; ++i) lp[i] *= fac[i];
+                }
+                uint32_t hi[RN / 4], lo[RN / 4];
+#pragma unroll
+                for (int i = 0; i < RN; i += 4) {
+                    const float4 R4 = *reinterpret_cast<const float4*>(ref_out + i);
+                    const float Rs[4] = {R4.x, R4.y, R4.z, R4.w};
+                    float v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // a row without any visible token yet has R = -inf and y = -inf: P = 0
+                        v[k] = ex2_approx(Rs[k] == -CUDART_INF_F ? (y[i + k] != y[i + k] ? y[i + k] : -CUDART_INF_F) : y[i + k] - Rs[k]);
+                        lp[i + k] = fmaf(v[k], inv_s, lp[i + k]);
+                    }
+                    split4_p(v[0], v[1], v[2], v[3], dither, dither, hi[i / 4], lo[i / 4]);
+                }
+                ok = mbar_wait(&bars[kBPFree + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
+                // row r, token tk: byte tk % 16 of the 16-byte unit tk / 16, at (unit ^ (row % 8)) of its 128-byte row
+                uint8_t* pb = smem + L::kOffP + sb * L::kPBytes + (tk & 15);
+#pragma unroll
+                for (int i = 0; i < RN; ++i) {
+                    const int r = row0 + i;
+                    uint8_t* at = pb + r * 128 + (((tk >> 4) ^ (r & 7)) << 4);
+                    at[0] = static_cast<uint8_t>(hi[i / 4] >> (8 * (i & 3)));
+                    at[NR * 128] = static_cast<uint8_t>(lo[i / 4] >> (8 * (i & 3)));  // (NR is a multiple of 8: the same place)
+                }
+                if (lane < RN) reinterpret_cast<int8_t*>(smem + L::kOffD)[(4 * sb + qd) * NR + row0 + lane] = static_cast<int8_t>(d);
+                fence_proxy_async_cta();
+                mbar_arrive(&bars[kBPReady + sb]);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok) break;
+            // the rows' sums over this warp's tokens, with the references they are relative to, once the previous segment's
+            // have been read
+            if (kseg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars[kBOFree], (kseg - 1) & 1u, abort_flag, kLimitNs));
+            if (!ok) break;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < RN; ++i) {
+                float v = lp[i];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == i) sum = v;
+            }
+            if (lane < RN) reinterpret_cast<float2*>(smem + L::kOffL)[warp * RN + lane] = make_float2(sum, ref.R);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kBLReady]);
+            ++kseg;
+        }
+        if (!ok) raise_abort(abort_flag, p.dev_status);
+    } else if (warp >= kWarpEpi) {
+        // ---- rescaling and output: warps 12..15, lane = latent column 128 c + 32 qd + lane of block c
+        const int qd = warp & 3;
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
+        SegWalk w = walk;
+        Seg s;
+        uint32_t kseg = 0, nresc = 0;
+        bool ok = true;
+        while (ok && w.next(p, s)) {
+            const uint64_t t0 = globaltimer_ns();
+            uint32_t it = 0;
+            for (;;) {
+                int ev = 0;  // 1: O^T complete, 2: rescale request, 3: give up
+                if (lane == 0) {
+                    if (mbar_test(smem_u32(&bars[kBOFull]), kseg & 1u)) ev = 1;
+                    else if (mbar_test(smem_u32(&bars[kBRescReq]), nresc & 1u)) ev = 2;
+                    else if (*abort_flag) ev = 3;
+                    else if ((++it & 255u) == 0 && globaltimer_ns() - t0 > kLimitNs) ev = 3;
+                }
+                ev = __shfl_sync(0xffffffffu, ev, 0);
+                if (ev == 1) {
+                    ok = mbar_wait(&bars[kBOFull], kseg & 1u, abort_flag, kLimitNs) &&
+                         mbar_wait(&bars[kBLReady], kseg & 1u, abort_flag, kLimitNs);
+                    break;
+                }
+                if (ev == 3) {
+                    ok = false;
+                    break;
+                }
+                if (ev == 2) {
+                    ok = mbar_wait(&bars[kBRescReq], nresc & 1u, abort_flag, kLimitNs) &&
+                         mbar_wait(&bars[kBODrain], nresc & 1u, abort_flag, kLimitNs);
+                    __syncwarp();
+                    tc_fence_after();
+                    const int8_t* dd = reinterpret_cast<const int8_t*>(smem + L::kOffD + *resc_at);
+#pragma unroll 1
+                    for (int c = 0; c < 4 * L::kOC; c += 8) {
+                        uint32_t v[8];
+                        tmem_ld8(t_lane + L::col_o(0) + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = __float_as_uint(__uint_as_float(v[k]) * RowRef::factor(dd[(c + k) % NR]));
+                        tmem_st8(t_lane + L::col_o(0) + c, v);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&bars[kBRescDone]);
+                    ++nresc;
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    continue;
+                }
+                __nanosleep(128);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            __syncwarp();
+            if (!ok) break;
+            tc_fence_after();
+            // (R, l) per row: R only rises, so the last unit's is the largest of the four warps'
+            for (int r = 32 * qd + lane; r < p.R; r += 128) {
+                const float2* part = reinterpret_cast<const float2*>(smem + L::kOffL) + (r / RN) * 4 * RN + r % RN;
+                const float2 a = part[0], b = part[RN], c = part[2 * RN], d = part[3 * RN];
+                const float R = fmaxf(fmaxf(a.y, b.y), fmaxf(c.y, d.y));
+                const float l = a.x * RowRef::step(a.y, R) + b.x * RowRef::step(b.y, R) + c.x * RowRef::step(c.y, R) +
+                                d.x * RowRef::step(d.y, R);
+                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float2(l != l ? 0.f : R, l);
+            }
+            // the workspace holds [column group c / 4][row] x float4, rs rows per slot
+            float* oseg = p.o_part + static_cast<int64_t>(s.slot) * p.rs * kDc;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const int col = 128 * c + 32 * qd + lane;
+                float* to = oseg + ((col >> 2) * p.rs) * 4 + (col & 3);
+#pragma unroll 1
+                for (int r = 0; r < NR; r += 8) {
+                    uint32_t v[8], u[8];
+                    tmem_ld8(t_lane + L::col_o(c) + r, v);
+                    if (L::kStack) tmem_ld8(t_lane + L::col_o(c) + NR + r, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (r + k < p.R)
+                            to[4 * (r + k)] = __uint_as_float(v[k]) + (L::kStack ? __uint_as_float(u[k]) : 0.f);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[kBOFree]);
+            ++kseg;
+        }
+        if (!ok && lane == 0) raise_abort(abort_flag, p.dev_status);
+    }
+
+    // ------------------------------------------------------------------ teardown
+    grid_dependents_launch();  // the merge kernel may be scheduled; it waits for this grid to finish
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpProducer) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kTmemCols);
+    }
+}
+
+template <int NR>
+cudaError_t launch(const Params& prm, cudaStream_t stream) {
+    using L = Lay<NR>;
+    cudaError_t e = cudaFuncSetAttribute(decode8_sm_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(prm.P_g);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode8_sm_kernel<NR>, prm);
+}
+
+}  // namespace sm8
+
+cudaError_t launch_decode8_sm(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
+                              int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int ctas,
+                              float* o_part, float2* ml_part, int slots, int rs, int32_t* dev_status,
+                              cudaStream_t stream) {
+    const int R = n_q * H;
+    if (R < 1 || R > kMaxSm8Rows || R > rs || ctas < 1 || B + ctas > slots) return cudaErrorInvalidValue;
+    const d8::Params prm = {q, cache, block_table, kv_len, o_part, ml_part, dev_status, cap_blocks, max_blocks, B, n_q, H, R,
+                            1, ctas, slots, rs, scale * 1.44269504088896340736f};
+    if (R <= 16) return sm8::launch<16>(prm, stream);
+    return R <= 32 ? sm8::launch<32>(prm, stream) : sm8::launch<48>(prm, stream);
+}
+
+}  // namespace mla

@@ -84,13 +84,16 @@ int tc_clusters_per_group(int G, int num_splits, bool one_sm) {
 
 // Decode over the 8-bit cache: work units per group of 128 query rows, and the same workspace regions.  Units do not
 // wait on one another, so their number need not be what the device holds at once.
-int units8(int n_q, int H) { return max_pairs_per_group((n_q * H + 127) / 128); }
+bool one_sm8(int n_q, int H) { return static_cast<int64_t>(n_q) * H <= kMaxSm8Rows; }
+int units8(int n_q, int H) {
+    return one_sm8(n_q, H) ? kMaxSmCtas : max_pairs_per_group((n_q * H + 127) / 128);
+}
 
 TcWs ws8_layout(int B, int n_q, int H) {
     TcWs w;
     w.G = (n_q * H + 127) / 128;
     w.slots = B + units8(n_q, H);
-    w.rs = 128;
+    w.rs = one_sm8(n_q, H) ? (n_q * H <= 32 ? 32 : 64) : 128;
     const size_t rows = static_cast<size_t>(w.G) * w.slots * w.rs;
     w.ml_part = 0;
     w.o_part = align1k(rows * sizeof(float2));
@@ -272,9 +275,13 @@ mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, co
     float2* ml_part = reinterpret_cast<float2*>(ws + lay.ml_part);
     uint8_t* olat = reinterpret_cast<uint8_t*>(ws + lay.olat);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_decode8_tc(static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(cache8), cap_blocks,
-                                      block_table, max_blocks, kv_len, B, n_q, H, scale, units, o_part, ml_part,
-                                      lay.slots, dev_status, cs);
+    const uint16_t* qp = static_cast<const uint16_t*>(q);
+    const uint8_t* cp = static_cast<const uint8_t*>(cache8);
+    cudaError_t e = one_sm8(n_q, H)
+                        ? launch_decode8_sm(qp, cp, cap_blocks, block_table, max_blocks, kv_len, B, n_q, H, scale, units,
+                                            o_part, ml_part, lay.slots, lay.rs, dev_status, cs)
+                        : launch_decode8_tc(qp, cp, cap_blocks, block_table, max_blocks, kv_len, B, n_q, H, scale, units,
+                                            o_part, ml_part, lay.slots, dev_status, cs);
     if (e == cudaSuccess)
         e = launch_merge(o_part, ml_part, kv_len, max_blocks, B, n_q, H, units, lay.slots, lay.rs, olat, lse_out,
                          dev_status, cs, true);

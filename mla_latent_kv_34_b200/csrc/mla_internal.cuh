@@ -25,6 +25,7 @@ constexpr int kBlock8Chunk = kBlockTokens * 128;
 constexpr int kBlock8Rope = 4 * kBlock8Chunk;
 constexpr int kBlock8Scales = kBlock8Rope + kBlockTokens * kDr;
 static_assert(kBlock8Bytes == kBlock8Scales + kBlockTokens * 4, "8-bit block layout");
+constexpr int kMaxSm8Rows = 48;    // query rows up to which the 8-bit decode runs on one SM per work unit
 constexpr int kScale8MinExp = -40;  // smallest scale of a row: 2^-40
 constexpr int kMaxPairs = 74;      // CTA pairs per row group the tensor-core decode uses at most (148 SMs / 2)
 constexpr int kMaxSmRows = 32;     // query rows (n_q * H) up to which the one-SM decode kernel runs instead
@@ -125,10 +126,15 @@ cudaError_t launch_decode_tc(const uint16_t* q, const uint8_t* cache, int64_t ca
                              int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale,
                              int clusters_per_group, float* o_part, float2* ml_part, int slots, int32_t* dev_status,
                              cudaStream_t stream);
-// Attend phase over the 8-bit cache (decode8_tc.cu): P_g CTA pairs per group of 128 query rows.
+// Attend phase over the 8-bit cache: P_g CTA pairs per group of 128 query rows (decode8_tc.cu), or one SM per work unit
+// for at most kMaxSm8Rows rows (decode8_sm.cu).
 cudaError_t launch_decode8_tc(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
                               int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int P_g,
                               float* o_part, float2* ml_part, int slots, int32_t* dev_status, cudaStream_t stream);
+cudaError_t launch_decode8_sm(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
+                              int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int ctas,
+                              float* o_part, float2* ml_part, int slots, int rs, int32_t* dev_status,
+                              cudaStream_t stream);
 // Rows of the merged latent output o_lat kept for the up-projection: T rounded so that every 64-token
 // block but the last is full and the last is a multiple of 16 (the MMA N granularity).
 __host__ __device__ __forceinline__ int olat_rows(int T) {
