@@ -185,12 +185,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
-// The lower byte to add to each fp16 of a pair before its upper byte is taken: half a step (rounding to nearest) where
-// the probability is at least 2^-6, the given dither where it is smaller.
-__device__ __forceinline__ uint32_t round_bytes(uint32_t p01, uint32_t dither) {
+// What to add to each fp16 of a pair before its lower bits are cut off: `half` a step (rounding to nearest) where the
+// probability is at least 2^-6, the given dither where it is smaller.
+__device__ __forceinline__ uint32_t round_term(uint32_t p01, uint32_t dither, uint32_t half) {
     const __half2 least = __halves2half2(__ushort_as_half(0x2400), __ushort_as_half(0x2400));  // 2^-6
     const uint32_t small = __hlt2_mask(*reinterpret_cast<const __half2*>(&p01), least);
-    return (small & dither) | (~small & 0x00800080u);
+    return (small & dither) | (~small & half);
 }
 
 // Four probabilities 0 <= p <= 2^8.75 as hi (e4m3) and lo (e5m2) codes.  hi rounds to nearest; lo is what is left, in
@@ -209,7 +209,26 @@ __device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3,
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d01) : "r"(h01), "r"(e4m3x2_to_f16x2(a)));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
     hi = a | (static_cast<uint32_t>(b) << 16);
-    lo = __byte_perm(d01 + round_bytes(h01, dither01), d23 + round_bytes(h23, dither23), 0x7531);
+    lo = __byte_perm(d01 + round_term(h01, dither01, 0x00800080u), d23 + round_term(h23, dither23, 0x00800080u), 0x7531);
+}
+// The same with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant bits down
+// to 2^-10 and steps of 2^-13 below, dithered alike (`dither`: seven bits for each half).  An e4m3 code of x has the bits
+// of the fp16 of 2^-8 x, less its top exponent bit and its last seven.
+__device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+    uint32_t h01, h23, d01, d23;
+    uint16_t a, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h23) : "f"(p3), "f"(p2));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h01));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(h23));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d01) : "r"(h01), "r"(e4m3x2_to_f16x2(a)));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d01) : "r"(0x2C002C00u));  // 2^-4
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d23) : "r"(0x2C002C00u));
+    d01 += round_term(h01, dither, 0x00400040u);
+    d23 += round_term(h23, dither, 0x00400040u);
+    hi = a | (static_cast<uint32_t>(b) << 16);
+    lo = __byte_perm(((d01 << 1) & 0x7F007F00u) | (d01 & 0x80008000u), ((d23 << 1) & 0x7F007F00u) | (d23 & 0x80008000u), 0x7531);
 }
 // The dither of token pair k of a thread's row part: two bytes of a low-discrepancy sequence (multiples of the golden
 // ratio), one in each half's lower byte.
@@ -220,8 +239,7 @@ __host__ __device__ constexpr uint32_t dither_pair(int k) {
 
 // The reference exponent of a row's probabilities, P' = 2^(y - R) with y = log2(p s_t) (s_t, the token's scale, is
 // folded into P because V's rows are codes).  O and the sum are kept relative to R, an integer, so moving it multiplies
-// them by an exact power of two.  P' has to stay below 448 (e4m3): R moves up when a tile's largest y - R exceeds 8.75,
-// and then (as at a piece's first tile) to where the largest P' lies in (1, 2].  It need not move down: a probability
+// them by an exact power of two.  P' has to stay below 448 (e4m3): R moves up when a unit's largest y - R exceeds 8.75, and then (as at a piece's first tile) to where the largest P' lies in (1, 2].  It need not move down: a probability
 // 2^-20 of the largest is still held by split4_p, and 2^17 tokens below that are less than 1/8 of the sum.
 struct RowRef {
     float R;

@@ -3,16 +3,17 @@
 // The attend phase of mla_decode8, with both contractions transposed, the 128 tokens of a block as the M side:
 //   S^T[token, row] = K . [Q_hi | Q_lo]^T   M = 128 tokens (A: the block's codes as they lie), N = 2 NR: 18 MMAs
 //   O^T[latent, row] += V^T . [P_hi | P_lo]^T   M = 128 latent columns per block of four (A: the same codes, MN-major),
-//                                           K = 128 tokens in steps of 32: 16 MMAs of N = 2 NR (hi and lo in columns of
-//                                           their own, added at the end), or 32 of N = NR where that does not fit
+//                                           K = 128 tokens in steps of 32: 16 MMAs of N = 2 NR (hi and lo * 2^4 in
+//                                           columns of their own, added at the end), or, where those do not fit, 32 of
+//                                           N = NR (lo as e5m2)
 // (NR: the rows rounded up to 16, 32 or 48).  Scores and O^T fit one SM's tensor memory, so a block is read once, by one
 // SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token, 1.67 us a block and SM with all SMs reading; the
 // MMAs of a block take about half of that, and a ring of two blocks keeps the reads going (the bf16 kernel's ring holds
 // one, and its reads wait for its MMAs).
 //
-// Softmax: a thread per token (tensor-memory lane) and half the rows.  The four warps of a set take 32 tokens each, a
-// unit; they hand the rows' reference exponents on (RowRef in decode8_common.cuh), so no barrier holds them in step.  A
-// row's maximum over a unit is a warp reduction; the token's scale is one register.
+// Softmax: a thread per token (tensor-memory lane) and half the rows; a set of four warps has a tile's 128 tokens.  A row's
+// maximum over a warp's tokens is a warp reduction, then the set's warps exchange them at one barrier and each decides on
+// the reference exponent (RowRef in decode8_common.cuh) by itself; the token's scale is one register.
 //
 // Warps: 0..7 softmax (set = warp / 4), 8 copies, 9 MMAs, 12..15 rescaling of O^T and a segment's output.  Scheduling and
 // output are the pair kernel's (decode8_tc.cu).  Every wait is bounded.
@@ -32,9 +33,10 @@ constexpr int kSoftWarps = 8, kSoftThreads = 256;
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpEpi = 12;
 constexpr int kThreads = 512;
 
-constexpr int kBFull = 0, kBEmpty = 4, kBSFull = 8, kBSEmpty = 10, kBPReady = 12, kBPFree = 14, kBRef = 16, kBQReady = 24,
-              kBOFull = 25, kBOFree = 26, kBRescReq = 27, kBRescDone = 28, kBODrain = 29, kBLReady = 30, kBFin = 31,
-              kNumBars = 32;
+constexpr uint32_t kNbSet = 1;  // named barriers 1, 2: the four softmax warps of a set
+
+constexpr int kBFull = 0, kBEmpty = 4, kBSFull = 8, kBSEmpty = 10, kBPReady = 12, kBPFree = 14, kBQReady = 16, kBOFull = 17,
+              kBOFree = 18, kBRescReq = 19, kBRescDone = 20, kBODrain = 21, kBLReady = 22, kBFin = 23, kNumBars = 24;
 
 template <int NR>
 struct Lay {
@@ -48,11 +50,11 @@ struct Lay {
     static constexpr int kOffQ = 2 * kTileBytes;             // four chunks, then the RoPE columns (64 bytes a row)
     static constexpr int kOffP = kOffQ + 4 * kQChunk + kN * 64;
     static constexpr int kPBytes = kN * 128;                 // [hi rows | lo rows] x 128 tokens, swizzled
-    static constexpr int kOffD = kOffP + 2 * kPBytes;        // [2 buffers][4 units][NR] int8 rescale exponents
-    static constexpr int kOffRowF = kOffD + 8 * NR;          // [NR] fp32: 2^a scale log2 e
-    static constexpr int kOffRef = kOffRowF + 4 * NR;        // [8 warps][kRN] reference exponents
-    static constexpr int kOffFac = kOffRef + 8 * kRN * 4;    // [8 warps][kRN] factors of the sums
-    static constexpr int kOffL = kOffFac + 8 * kRN * 4;      // [8 warps][kRN] (sum, reference) of a segment
+    static constexpr int kOffD = kOffP + 2 * kPBytes;        // [2 buffers][NR] int8 rescale exponents
+    static constexpr int kOffRowF = kOffD + 2 * NR;          // [NR] fp32: 2^a scale log2 e
+    static constexpr int kOffMax = kOffRowF + 4 * NR;        // [2 tiles][8 warps][kRN] row maxima
+    static constexpr int kOffRef = kOffMax + 16 * kRN * 4;   // [8 warps][kRN] reference exponents, as the warp broadcasts them
+    static constexpr int kOffL = kOffRef + 8 * kRN * 4;      // [8 warps][kRN] (sum, reference) of a segment
     static constexpr int kOffBar = kOffL + 8 * kRN * 8;
     static constexpr int kOffTail = kOffBar + kNumBars * 8;  // tmem base, abort flag, rescale place, [total, sequence, tile]
     static constexpr int kSmemBytes = kOffTail + 32;
@@ -117,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             mbar_init(&bars[kBPReady + i], kSoftThreads);
             mbar_init(&bars[kBPFree + i], 1);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&bars[kBRef + i], 1);
         mbar_init(&bars[kBQReady], kSoftThreads);
         mbar_init(&bars[kBOFull], 1);
         mbar_init(&bars[kBOFree], 128);
@@ -181,10 +182,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
-        // ---- MMA issuer: the scores of a tile go out before the tile before it is aggregated
+        // ---- MMA issuer: the scores of a tile go out as soon as it is there, its aggregation as soon as P is: whichever of
+        //      the next two is ready first (waiting for a copy with a P at hand would hold that tile's slot, and the copy
+        //      that wants it)
         const bool leader = elect_one();
+        const uint32_t tm = uniform(tmem);
         constexpr uint32_t idesc_s = idesc_f8_f32(128, L::kN, false, false);
-        constexpr uint32_t idesc_hi = idesc_f8_f32(128, NR, true, false);
+        constexpr uint32_t idesc_hi = idesc_f8_f32(128, L::kStack ? L::kN : NR, true, false);
         constexpr uint32_t idesc_lo = idesc_f8_f32(128, NR, true, false, false, true);
         const uint64_t k_desc = sdesc_sw128(sbase + L::kOffRing, 16, 1024);            // K-major chunks
         const uint64_t kr_desc = sdesc_sw64(sbase + L::kOffRing + kBlock8Rope, 16, 512);
@@ -194,23 +198,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
         const uint64_t p_desc = sdesc_sw128(sbase + L::kOffP, 16, 1024);
         SegWalk w = walk;
         Seg s;
-        uint32_t n = 0, kseg = 0, nresc = 0;
+        uint32_t n0 = 0, kseg = 0, nresc = 0;  // tiles of the segments before
         bool ok = true;
         while (ok && w.next(p, s)) {
             if (leader) ok = mbar_wait(&bars[kBQReady], kseg & 1u, abort_flag, kLimitNs);
             ok = __any_sync(0xffffffffu, ok && leader);
-            // step t issues the scores of tile t and aggregates tile t - 1
-            for (int t = s.t0; ok && t <= s.t1; ++t, ++n) {
-                if (t < s.t1) {
-                    const uint32_t sb = n & 1u, us = n >> 1;
-                    const int nvalid = min(kTile, s.L - t * kTile);
-                    if (leader) {
-                        ok = mbar_wait(&bars[kBSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
-                        for (int k = 0; ok && k < 2; ++k)
-                            ok = mbar_wait(&bars[kBFull + 2 * sb + k], us & 1u, abort_flag, kLimitNs);
+            const uint32_t tiles = static_cast<uint32_t>(s.t1 - s.t0);
+            uint32_t is = 0, ip = 0;  // tiles whose scores are issued, tiles aggregated
+            while (ok && ip < tiles) {
+                const uint32_t n = n0 + is, sb = n & 1u, us = n >> 1;
+                const uint32_t m = n0 + ip, pb = m & 1u, um = m >> 1;
+                int what = 0;  // 1: scores of tile is, 2: aggregation of tile ip, 3: give up
+                if (leader) {
+                    uint64_t since = 0;
+                    uint32_t it = 0;
+                    while (what == 0) {
+                        if (ip < is && mbar_poll(smem_u32(&bars[kBPReady + pb]), um & 1u)) what = 2;
+                        else if (is < tiles && is < ip + 2 && mbar_poll(smem_u32(&bars[kBSEmpty + sb]), (us & 1u) ^ 1u) &&
+                                 mbar_poll(smem_u32(&bars[kBFull + 2 * sb]), us & 1u) &&
+                                 mbar_poll(smem_u32(&bars[kBFull + 2 * sb + 1]), us & 1u))
+                            what = 1;
+                        else if ((++it & 255u) == 0) {
+                            const uint64_t now = globaltimer_ns();
+                            if (since == 0) since = now;
+                            if (*abort_flag || now - since > kLimitNs) what = 3;
+                        }
                     }
-                    ok = __any_sync(0xffffffffu, ok && leader);
-                    if (!ok) break;
+                    if (what == 2 && ip == 0 && !mbar_wait(&bars[kBOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs)) what = 3;
+                }
+                what = __reduce_max_sync(0xffffffffu, leader ? what : 0);
+                if (what == 3) {
+                    ok = false;
+                    break;
+                }
+                if (what == 1) {
+                    const int nvalid = min(kTile, s.L - (s.t0 + static_cast<int>(is)) * kTile);
                     if (nvalid < kTile) {
                         // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN); their scores are masked
                         const int nz = (kTile - nvalid) * 8;  // 16-byte units per chunk
@@ -222,10 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                         fence_proxy_async_cta();
                     }
                     __syncwarp();
-                    if (leader) {
+                    const uint32_t sbu = uniform(sb);
+                    if (elect_one()) {
                         tc_fence_after();
-                        const uint64_t off = static_cast<uint64_t>(sb * kTileBytes) >> 4;
-                        const uint32_t d = tmem + L::col_s(sb);
+                        const uint64_t off = static_cast<uint64_t>(sbu * kTileBytes) >> 4;
+                        const uint32_t d = tm + L::col_s(sbu);
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -234,64 +257,48 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                                         idesc_s, (c | kk) ? 1u : 0u);
                         mma8_ss(d, kr_desc + off, qr_desc, idesc_s, 1u);
                         mma8_ss(d, kr_desc + off + 2, qr_desc + 2, idesc_s, 1u);
-                        mma_commit(smem_u32(&bars[kBSFull + sb]));
+                        mma_commit(smem_u32(&bars[kBSFull + sbu]));
                     }
                     __syncwarp();
+                    ++is;
+                    continue;
                 }
-                if (t > s.t0) {
-                    const uint32_t m = n - 1, pb = m & 1u, um = m >> 1;
-                    const bool seg_first = (t - 1 == s.t0);
+                if (ip > 0 && __any_sync(0xffffffffu, 4 * lane < NR && reinterpret_cast<const uint32_t*>(
+                                                                           smem + L::kOffD + pb * NR)[lane] != 0)) {
+                    // some row's reference moved: have O^T rescaled once all earlier MMAs are done
                     if (leader) {
-                        ok = mbar_wait(&bars[kBPReady + pb], um & 1u, abort_flag, kLimitNs);
-                        if (ok && seg_first) ok = mbar_wait(&bars[kBOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs);
+                        *resc_at = static_cast<int>(pb * NR);
+                        mma_commit(smem_u32(&bars[kBODrain]));
+                        mbar_arrive(&bars[kBRescReq]);
+                        ok = mbar_wait(&bars[kBRescDone], nresc & 1u, abort_flag, kLimitNs);
                     }
+                    ++nresc;
                     ok = __any_sync(0xffffffffu, ok && leader);
                     if (!ok) break;
-#pragma unroll 1
-                    for (int u = 0; u < 4; ++u) {
-                        const bool fresh = seg_first && u == 0;
-                        const uint8_t* moved = smem + L::kOffD + (4 * pb + u) * NR;
-                        const bool resc = __any_sync(0xffffffffu, 4 * lane < NR && reinterpret_cast<const uint32_t*>(moved)[lane] != 0);
-                        if (!fresh && resc) {
-                            // some row's reference moved: have O^T rescaled once all earlier MMAs are done
-                            if (leader) {
-                                *resc_at = static_cast<int>((4 * pb + u) * NR);
-                                mma_commit(smem_u32(&bars[kBODrain]));
-                                mbar_arrive(&bars[kBRescReq]);
-                                ok = mbar_wait(&bars[kBRescDone], nresc & 1u, abort_flag, kLimitNs);
-                            }
-                            ++nresc;
-                            ok = __any_sync(0xffffffffu, ok && leader);
-                            if (!ok) break;
-                        }
-                        if (leader) {
-                            tc_fence_after();
-                            const uint64_t v = v_desc + (static_cast<uint64_t>(pb * kTileBytes + u * 4096) >> 4);
-                            const uint64_t pd = p_desc + (static_cast<uint64_t>(pb * L::kPBytes + u * 32) >> 4);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t o = tmem + L::col_o(c);
-                                const uint64_t vc = v + ((c * kChunk) >> 4);
-                                mma8_ss(o, vc, pd, idesc_hi, fresh ? 0u : 1u);
-                                mma8_ss(L::kStack ? o + NR : o, vc, pd + ((NR * 128) >> 4), idesc_lo,
-                                        (L::kStack && fresh) ? 0u : 1u);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
-                    if (leader) {
-                        mma_commit(smem_u32(&bars[kBEmpty + 2 * pb]));
-                        mma_commit(smem_u32(&bars[kBEmpty + 2 * pb + 1]));
-                        mma_commit(smem_u32(&bars[kBPFree + pb]));
-                    }
-                    __syncwarp();
                 }
+                const uint32_t pbu = uniform(pb), accum = uniform(ip > 0 ? 1u : 0u);
+                if (elect_one()) {
+                    tc_fence_after();
+                    const uint64_t v = v_desc + (static_cast<uint64_t>(pbu * kTileBytes) >> 4);
+                    const uint64_t pd = p_desc + (static_cast<uint64_t>(pbu * L::kPBytes) >> 4);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t o = tm + L::col_o(c);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const uint64_t vc = v + ((c * kChunk + u * 4096) >> 4);
+                            mma8_ss(o, vc, pd + 2 * u, idesc_hi, u ? 1u : accum);
+                            if (!L::kStack) mma8_ss(o, vc, pd + 2 * u + ((NR * 128) >> 4), idesc_lo, 1u);
+                        }
+                        if (c & 1) mma_commit(smem_u32(&bars[kBEmpty + 2 * pbu + (c >> 1)]));
+                    }
+                    mma_commit(smem_u32(&bars[kBPFree + pbu]));
+                    if (ip + 1 == tiles) mma_commit(smem_u32(&bars[kBOFull]));
+                }
+                __syncwarp();
+                ++ip;
             }
-            --n;  // (the last step issued no scores)
-            if (!ok) break;
-            if (leader) mma_commit(smem_u32(&bars[kBOFull]));
-            __syncwarp();
+            n0 += tiles;
             ++kseg;
         }
         if (!ok && leader) raise_abort(abort_flag, p.dev_status);
@@ -305,17 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
         const int qd = warp & 3, set = warp >> 2, row0 = set * RN;
         const int tk = 32 * qd + lane;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
-        volatile float* ref_in = reinterpret_cast<volatile float*>(smem + L::kOffRef) + (4 * set + ((qd + 3) & 3)) * RN;
-        float* ref_out = reinterpret_cast<float*>(smem + L::kOffRef) + warp * RN;
-        float* fac = reinterpret_cast<float*>(smem + L::kOffFac) + warp * RN;
-        uint64_t* bar_in = &bars[kBRef + 4 * set + ((qd + 3) & 3)];
-        uint64_t* bar_out = &bars[kBRef + warp];
+        float* refs = reinterpret_cast<float*>(smem + L::kOffRef) + warp * RN;
         const float* rowf_all = reinterpret_cast<const float*>(smem + L::kOffRowF);
         // the token's dither (multiples of the golden ratio over the tokens), for both halves of a pair of rows
         const uint32_t dither = (((static_cast<uint32_t>(tk) * 40503u + 20251u) >> 8) & 0xFFu) * 0x00010001u;
         SegWalk w = walk;
         Seg s;
-        uint32_t n = 0, kseg = 0, nref = 0;
+        uint32_t n = 0, kseg = 0;
         bool ok = true;
         while (ok && w.next(p, s)) {
             // the token's scale in the tiles to come, a tile ahead (the table entry two ahead)
@@ -427,37 +430,34 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     for (int i = 0; i < RN; ++i)
                         if (tok >= lim0 + (row0 + i) / p.H) y[i] = -CUDART_INF_F;
                 }
-                // the unit's row maxima: lane i gets row row0 + i's
+                // the tile's row maxima: lane i gets row row0 + i's over the warp's tokens, then over the set's
                 float top = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < RN; ++i) {
                     const float v = warp_max_f32(y[i]);
                     if (lane == i) top = v;
                 }
-                if (row0 + lane >= p.R) top = -CUDART_INF_F;  // rows of no query: P = 0 (y = -inf below)
-                // the references: the previous unit's (another warp's), moved where this unit needs it, handed on
-                const float last = ref.R;
-                if (qd > 0 || t > s.t0) {
-                    ok = mbar_wait(bar_in, nref & 1u, abort_flag, kLimitNs) && ok;
-                    ++nref;
-                    if (lane < RN) ref.R = ref_in[lane];
+                float* mx = reinterpret_cast<float*>(smem + L::kOffMax) + (8 * sb + 4 * set) * RN;
+                if (lane < RN) mx[qd * RN + lane] = top;
+                if (bar_red_or(kNbSet + set, 128, !ok || *abort_flag != 0)) {
+                    ok = false;
+                    break;
                 }
+                // (rows of no query keep R = -inf: P = 0)
+                if (lane < RN && row0 + lane < p.R)
+                    top = fmaxf(fmaxf(mx[lane], mx[RN + lane]), fmaxf(mx[2 * RN + lane], mx[3 * RN + lane]));
+                else top = -CUDART_INF_F;
                 const int d = ref.move(top);
-                const float step = RowRef::step(last, ref.R);
-                if (lane < RN) {
-                    ref_out[lane] = ref.R;
-                    fac[lane] = step;
-                }
-                __syncwarp();
-                if (lane == 0 && (qd < 3 || t + 1 < s.t1)) mbar_arrive(bar_out);
-                if (__any_sync(0xffffffffu, lane < RN && step != 1.f)) {
+                if (__any_sync(0xffffffffu, d != 0)) {
 #pragma unroll
-                    for (int i = 0; i < RN; ++i) lp[i] *= fac[i];
+                    for (int i = 0; i < RN; ++i) lp[i] *= RowRef::factor(__shfl_sync(0xffffffffu, d, i));
                 }
+                if (lane < RN) refs[lane] = ref.R;
+                __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
                 for (int i = 0; i < RN; i += 4) {
-                    const float4 R4 = *reinterpret_cast<const float4*>(ref_out + i);
+                    const float4 R4 = *reinterpret_cast<const float4*>(refs + i);
                     const float Rs[4] = {R4.x, R4.y, R4.z, R4.w};
                     float v[4];
 #pragma unroll
@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                         v[k] = ex2_approx(Rs[k] == -CUDART_INF_F ? (y[i + k] != y[i + k] ? y[i + k] : -CUDART_INF_F) : y[i + k] - Rs[k]);
                         lp[i + k] = fmaf(v[k], inv_s, lp[i + k]);
                     }
-                    split4_p(v[0], v[1], v[2], v[3], dither, dither, hi[i / 4], lo[i / 4]);
+                    if (L::kStack) split4_p16(v[0], v[1], v[2], v[3], (dither >> 1) & 0x007F007Fu, hi[i / 4], lo[i / 4]);
+                    else split4_p(v[0], v[1], v[2], v[3], dither, dither, hi[i / 4], lo[i / 4]);
                 }
                 ok = mbar_wait(&bars[kBPFree + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
                 // row r, token tk: byte tk % 16 of the 16-byte unit tk / 16, at (unit ^ (row % 8)) of its 128-byte row
@@ -478,14 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     at[0] = static_cast<uint8_t>(hi[i / 4] >> (8 * (i & 3)));
                     at[NR * 128] = static_cast<uint8_t>(lo[i / 4] >> (8 * (i & 3)));  // (NR is a multiple of 8: the same place)
                 }
-                if (lane < RN) reinterpret_cast<int8_t*>(smem + L::kOffD)[(4 * sb + qd) * NR + row0 + lane] = static_cast<int8_t>(d);
+                if (qd == 0 && lane < RN) reinterpret_cast<int8_t*>(smem + L::kOffD)[sb * NR + row0 + lane] = static_cast<int8_t>(d);
                 fence_proxy_async_cta();
                 mbar_arrive(&bars[kBPReady + sb]);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
             }
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             // the rows' sums over this warp's tokens, with the references they are relative to, once the previous segment's
             // have been read
@@ -541,14 +539,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     tc_fence_after();
                     const int8_t* dd = reinterpret_cast<const int8_t*>(smem + L::kOffD + *resc_at);
 #pragma unroll 1
-                    for (int c = 0; c < 4 * L::kOC; c += 8) {
-                        uint32_t v[8];
-                        tmem_ld8(t_lane + L::col_o(0) + c, v);
-                        tmem_wait_ld();
+                    for (int r = 0; r < NR; r += 8) {
+                        float f[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            v[k] = __float_as_uint(__uint_as_float(v[k]) * RowRef::factor(dd[(c + k) % NR]));
-                        tmem_st8(t_lane + L::col_o(0) + c, v);
+                        for (int k = 0; k < 8; ++k) f[k] = RowRef::factor(dd[r + k]);
+#pragma unroll
+                        for (int part = 0; part < L::kOC / NR; ++part) {  // hi columns, lo columns
+                            uint32_t v[4][8];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) tmem_ld8(t_lane + L::col_o(c) + part * NR + r, v[c]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) v[c][k] = __float_as_uint(__uint_as_float(v[c][k]) * f[k]);
+                                tmem_st8(t_lane + L::col_o(c) + part * NR + r, v[c]);
+                            }
+                        }
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -560,20 +567,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     }
                     continue;
                 }
-                __nanosleep(128);
+                __nanosleep(64);
             }
             ok = __all_sync(0xffffffffu, ok);
             __syncwarp();
             if (!ok) break;
             tc_fence_after();
-            // (R, l) per row: R only rises, so the last unit's is the largest of the four warps'
+            // (R, l) per row: the set's four warps ended with the same reference
             for (int r = 32 * qd + lane; r < p.R; r += 128) {
                 const float2* part = reinterpret_cast<const float2*>(smem + L::kOffL) + (r / RN) * 4 * RN + r % RN;
                 const float2 a = part[0], b = part[RN], c = part[2 * RN], d = part[3 * RN];
-                const float R = fmaxf(fmaxf(a.y, b.y), fmaxf(c.y, d.y));
-                const float l = a.x * RowRef::step(a.y, R) + b.x * RowRef::step(b.y, R) + c.x * RowRef::step(c.y, R) +
-                                d.x * RowRef::step(d.y, R);
-                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float2(l != l ? 0.f : R, l);
+                const float l = (a.x + b.x) + (c.x + d.x);
+                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float2(l != l ? 0.f : a.y, l);
             }
             // the workspace holds [column group c / 4][row] x float4, rs rows per slot
             float* oseg = p.o_part + static_cast<int64_t>(s.slot) * p.rs * kDc;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         if (r + k < p.R)
-                            to[4 * (r + k)] = __uint_as_float(v[k]) + (L::kStack ? __uint_as_float(u[k]) : 0.f);
+                            to[4 * (r + k)] = L::kStack ? fmaf(__uint_as_float(u[k]), 0x1p-4f, __uint_as_float(v[k])) : __uint_as_float(v[k]);
                 }
             }
             tc_fence_before();

@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                                 ok = __any_sync(0xffffffffu, ok && leader);
                                 if (!ok) break;
                             }
-                            if (leader) {
+                            if (elect_one()) {
                                 tc_fence_after();
                                 const uint64_t v = v_desc + (static_cast<uint64_t>(st * kVBytes + (2 * h + kk) * (kUnit * 128)) >> 4);
                                 const uint64_t pd = p_desc + (static_cast<uint64_t>(pb * kMsgStride + kk * 32) >> 4);

@@ -91,6 +91,19 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t addr, uint32_t parity
     return ok != 0;
 }
 
+// The same without any wait of the hardware's own, for loops that look at several barriers.
+__device__ __forceinline__ bool mbar_poll(uint32_t addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // try_wait with a suspend-time hint: a waiting thread sleeps in hardware until the
 // phase completes (or the hint, in ns, runs out) instead of spinning on issue slots.
 __device__ __forceinline__ bool mbar_sleep_wait(uint32_t addr, uint32_t parity, uint32_t hint_ns) {
@@ -284,13 +297,18 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// One lane of a converged warp.  MMAs issued under this predicate cost the issuing thread about 10 cycles each; under a
-// comparison of the lane index, 58 (their operands then go to uniform registers one by one).
+// One lane of a converged warp, the same each time.  MMAs issued in a block under this predicate cost the issuing thread
+// about 10 cycles each; under a comparison of the lane index, or a copy of the predicate, 58 (their operands then go to
+// uniform registers one by one).
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e != 0;
 }
+
+// A value that is the same in every lane of a converged warp, as the compiler can see it: MMA operands computed from it
+// stay in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16 (bf16 in, fp32 accumulate).
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
