@@ -185,21 +185,21 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
-// What to add to each fp16 of a pair before its lower bits are cut off: `half` a step (rounding to nearest) where the
-// probability is at least 2^-6, the given dither where it is smaller.
-__device__ __forceinline__ uint32_t round_term(uint32_t p01, uint32_t dither, uint32_t half) {
-    const __half2 least = __halves2half2(__ushort_as_half(0x2400), __ushort_as_half(0x2400));  // 2^-6
-    const uint32_t small = __hlt2_mask(*reinterpret_cast<const __half2*>(&p01), least);
-    return (small & dither) | (~small & half);
+// What to add to each fp16 of a pair before its lower bits are cut off: `half` a step (rounding to nearest), or the dither
+// where `mask` is set.
+__device__ __forceinline__ uint32_t round_term(uint32_t mask, uint32_t dither, uint32_t half) {
+    return (mask & dither) | (~mask & half);
 }
 
 // Four probabilities 0 <= p <= 2^8.75 as hi (e4m3) and lo (e5m2) codes.  hi rounds to nearest; lo is what is left, in
 // e5m2's 3 significant bits: e5m2 is the upper half of an fp16, so an integer addition to the lower byte rounds it.  Down
-// to p = 2^-6 the pair holds p within 2^-8, like a bf16.  Below, hi's steps are 2^-9 and lo goes on to 2^-16; there the
-// rounding is dithered, over the tokens alike, so that many equal small probabilities (a long tail behind one dominant
-// token) keep their sum, which rounding to nearest would move by up to an eighth.
-__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t dither01, uint32_t dither23,
-                                         uint32_t& hi, uint32_t& lo) {
+// to p = 2^-6 the pair holds p within 2^-8, like a bf16.  Below, hi's steps are 2^-9 and lo goes on to 2^-16, and many
+// equal small probabilities (a long tail behind one dominant token) would move their sum by up to an eighth if each were
+// rounded to nearest.  So where all of a row's probabilities in a unit are below 1 (`mask`; the reference is another
+// unit's), lo's rounding is dithered, over the tokens alike, which keeps the sum; where one is above, its unit's tail is
+// too small beside it to matter.
+__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t mask, uint32_t dither01,
+                                         uint32_t dither23, uint32_t& hi, uint32_t& lo) {
     uint32_t h01, h23, d01, d23;
     uint16_t a, b;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
@@ -209,12 +209,13 @@ __device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3,
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d01) : "r"(h01), "r"(e4m3x2_to_f16x2(a)));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
     hi = a | (static_cast<uint32_t>(b) << 16);
-    lo = __byte_perm(d01 + round_term(h01, dither01, 0x00800080u), d23 + round_term(h23, dither23, 0x00800080u), 0x7531);
+    lo = __byte_perm(d01 + round_term(mask, dither01, 0x00800080u), d23 + round_term(mask, dither23, 0x00800080u), 0x7531);
 }
 // The same with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant bits down
-// to 2^-10 and steps of 2^-13 below, dithered alike (`dither`: seven bits for each half).  An e4m3 code of x has the bits
+// to 2^-10 and steps of 2^-13 below, dithered alike (`add01`, `add23`: what to add before the last seven bits are cut off).  An e4m3 code of x has the bits
 // of the fp16 of 2^-8 x, less its top exponent bit and its last seven.
-__device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t add01, uint32_t add23,
+                                           uint32_t& hi, uint32_t& lo) {
     uint32_t h01, h23, d01, d23;
     uint16_t a, b;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
@@ -225,8 +226,8 @@ __device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d01) : "r"(0x2C002C00u));  // 2^-4
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d23) : "r"(0x2C002C00u));
-    d01 += round_term(h01, dither, 0x00400040u);
-    d23 += round_term(h23, dither, 0x00400040u);
+    d01 += add01;
+    d23 += add23;
     hi = a | (static_cast<uint32_t>(b) << 16);
     lo = __byte_perm(((d01 << 1) & 0x7F007F00u) | (d01 & 0x80008000u), ((d23 << 1) & 0x7F007F00u) | (d23 & 0x80008000u), 0x7531);
 }
@@ -244,16 +245,15 @@ __host__ __device__ constexpr uint32_t dither_pair(int k) {
 struct RowRef {
     float R;
     __device__ __forceinline__ void reset() { R = __uint_as_float(0xFF800000u); }
-    // Takes a tile's largest y (-inf: nothing visible); returns the exponent by which O and the sum are to be multiplied
+    __device__ __forceinline__ bool must_move(float top) const { return top > R + 8.75f; }
+    // Takes a unit's largest y (-inf: nothing visible); returns the exponent by which O and the sum are to be multiplied
     // (<= -126: they vanish), 0 for none.
     __device__ __forceinline__ int move(float top) {
-        int d = 0;
-        if (top > R + 8.75f) {
-            const float to = ceilf(top) - 1.f;
-            // (no O yet: R is -inf, and nothing is multiplied)
-            d = (R == __uint_as_float(0xFF800000u)) ? 0 : static_cast<int>(fmaxf(R - to, -127.f));
-            R = to;
-        }
+        if (!must_move(top)) return 0;
+        const float to = ceilf(top) - 1.f;
+        // (no O yet: R is -inf, and nothing is multiplied)
+        const int d = (R == __uint_as_float(0xFF800000u)) ? 0 : static_cast<int>(fmaxf(R - to, -127.f));
+        R = to;
         return d;
     }
     __device__ __forceinline__ static float factor(int d) { return d <= -126 ? 0.f : exp2_int(d); }
@@ -262,6 +262,8 @@ struct RowRef {
         return from == __uint_as_float(0xFF800000u) ? 1.f : factor(static_cast<int>(fmaxf(from - to, -127.f)));
     }
     __device__ __forceinline__ float minus() const { return R == __uint_as_float(0xFF800000u) ? 0.f : -R; }
+    // All ones where a unit's probabilities are all below 1 (round_term's mask).
+    __device__ __forceinline__ uint32_t low(float top) const { return top < R ? 0xFFFFFFFFu : 0u; }
 };
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 operands (a_e5m2, b_e5m2: that one e5m2) and fp32 D.

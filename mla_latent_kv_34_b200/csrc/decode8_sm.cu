@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     for (int i = 0; i < RN; ++i) lp[i] *= RowRef::factor(__shfl_sync(0xffffffffu, d, i));
                 }
                 if (lane < RN) refs[lane] = ref.R;
+                const uint32_t lows = __ballot_sync(0xffffffffu, ref.low(top) != 0);
                 __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
@@ -466,8 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                         v[k] = ex2_approx(Rs[k] == -CUDART_INF_F ? (y[i + k] != y[i + k] ? y[i + k] : -CUDART_INF_F) : y[i + k] - Rs[k]);
                         lp[i + k] = fmaf(v[k], inv_s, lp[i + k]);
                     }
-                    if (L::kStack) split4_p16(v[0], v[1], v[2], v[3], (dither >> 1) & 0x007F007Fu, hi[i / 4], lo[i / 4]);
-                    else split4_p(v[0], v[1], v[2], v[3], dither, dither, hi[i / 4], lo[i / 4]);
+                    // (the four are one token's in four rows: the masks differ within a pair)
+                    uint32_t add[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t mask = ((lows >> (i + 2 * k)) & 1u ? 0x0000FFFFu : 0u) | ((lows >> (i + 2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+                        add[k] = L::kStack ? round_term(mask, (dither >> 1) & 0x007F007Fu, 0x00400040u) : round_term(mask, dither, 0x00800080u);
+                    }
+                    if (L::kStack) split4_p16(v[0], v[1], v[2], v[3], add[0], add[1], hi[i / 4], lo[i / 4]);
+                    else split4_p(v[0], v[1], v[2], v[3], 0xFFFFFFFFu, add[0], add[1], hi[i / 4], lo[i / 4]);
                 }
                 ok = mbar_wait(&bars[kBPFree + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
                 // row r, token tk: byte tk % 16 of the 16-byte unit tk / 16, at (unit ^ (row % 8)) of its 128-byte row

@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             SegWalk w = walk, wn;
             Seg s, sn;
             uint32_t n = 0, kseg = 0, nref = 0;  // tiles, segments, references received
+            uint32_t stg = cq >> 1, stg_phase = 1;  // the staging buffer of message 2 n + cq / 2, and the phase it is free in
             bool ok = true;
             bool have = w.next(p, s);
             while (ok && have) {
@@ -418,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 const int limB = gB < p.R ? s.L - p.n_q + gB / p.H + 1 : 0;
                 for (int t = s.t0; t < s.t1; ++t, ++n) {
                     const uint32_t sb = n & 1u, us = n >> 1;
-                    const uint32_t msg = 2 * n + (cq >> 1), stg = msg % kStages;
                     if (t == t_pf && have_next && row_ok)
                         for (int c = cq; c < 9; c += 4) prefetch_l2(nq + 128 * c);
                     const uint4* sw4 = reinterpret_cast<const uint4*>(smem + kSOffScale + (n % kScaleBufs) * kScaleBytes) + cb / 8;
@@ -475,11 +475,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         refA.R = ref_in[lane & 15];
                         refB.R = ref_in[16 + (lane & 15)];
                     }
-                    const int dA = refA.move(mA), dB = refB.move(mB);
+                    int dA = 0, dB = 0;
+                    if (__any_sync(0xffffffffu, refA.must_move(mA) || refB.must_move(mB))) {
+                        dA = refA.move(mA);
+                        dB = refB.move(mB);
+                    }
                     if (cq < 3 || t + 1 < s.t1) {
                         ref_out[lane] = lane < 16 ? refA.R : refB.R;
                         mbar_arrive(bar_out);
                     }
+                    // the sums are relative to the reference of this warp's last unit
+                    if (__any_sync(0xffffffffu, lastA != refA.R || lastB != refB.R)) {
+                        lA *= RowRef::step(lastA, refA.R);
+                        lB *= RowRef::step(lastB, refB.R);
+                    }
+                    const uint32_t lowA = refA.low(mA), lowB = refB.low(mB);
                     const float2 nA = make_float2(refA.minus(), refA.minus()), nB = make_float2(refB.minus(), refB.minus());
                     float2 sA = make_float2(0.f, 0.f), sB = sA;
                     uint32_t hiA[4], loA[4], hiB[4], loB[4];
@@ -496,19 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             a1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
                             sA = fma2(a0, i0, sA);
                             sA = fma2(a1, i1, sA);
-                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
+                            split4_p(a0.x, a0.y, a1.x, a1.y, lowA, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
                             float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
                             b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
                             b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
                             sB = fma2(b0, i0, sB);
                             sB = fma2(b1, i1, sB);
-                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
+                            split4_p(b0.x, b0.y, b1.x, b1.y, lowB, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
                         }
                     }
-                    // the sum is relative to the reference of this warp's last unit
-                    lA = fmaf(lA, RowRef::step(lastA, refA.R), sA.x + sA.y);
-                    lB = fmaf(lB, RowRef::step(lastB, refB.R), sB.x + sB.y);
-                    ok = mbar_wait(&bars[kSBarFree + stg], ((msg / kStages) & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
+                    lA += sA.x + sA.y;
+                    lB += sB.x + sB.y;
+                    ok = mbar_wait(&bars[kSBarFree + stg], stg_phase, abort_flag, kLimitNs) && ok;
                     // a row's 16 columns: the 16-byte unit (cb / 16) % 4 of its hi part and of its lo part
                     uint8_t* stage = smem + kSOffStage + stg * kMsgStride;
                     uint8_t* at = stage + (32 * qd + (lane & 15)) * 128;
@@ -521,6 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     reinterpret_cast<int8_t*>(stage + kPBytes)[(cq & 1) * kRows + r] = static_cast<int8_t>(lane < 16 ? dA : dB);
                     fence_proxy_async_cta();
                     mbar_arrive(&bars[kSBarStaged + stg]);
+                    stg += 2;
+                    if (stg >= kStages) {
+                        stg -= kStages;
+                        stg_phase ^= 1u;
+                    }
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
