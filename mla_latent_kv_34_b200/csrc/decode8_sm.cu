@@ -78,18 +78,6 @@ __device__ __forceinline__ float warp_max_f32(float v) {
     return r;
 }
 
-// N columns of this warp's 32 lanes (N = 8, 16, 24 or 32).
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p) {
     using L = Lay<NR>;
@@ -588,12 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 const float l = (a.x + b.x) + (c.x + d.x);
                 p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float2(l != l ? 0.f : a.y, l);
             }
-            // the workspace holds [column group c / 4][row] x float4, rs rows per slot
+            // the workspace holds [column / 32][row] x 32 fp32, rs rows per slot
             float* oseg = p.o_part + static_cast<int64_t>(s.slot) * p.rs * kDc;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                const int col = 128 * c + 32 * qd + lane;
-                float* to = oseg + ((col >> 2) * p.rs) * 4 + (col & 3);
+                float* to = oseg + ((4 * c + qd) * p.rs) * 32 + lane;
 #pragma unroll 1
                 for (int r = 0; r < NR; r += 8) {
                     uint32_t v[8], u[8];
@@ -603,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         if (r + k < p.R)
-                            to[4 * (r + k)] = L::kStack ? fmaf(__uint_as_float(u[k]), 0x1p-4f, __uint_as_float(v[k])) : __uint_as_float(v[k]);
+                            to[32 * (r + k)] = L::kStack ? fmaf(__uint_as_float(u[k]), 0x1p-4f, __uint_as_float(v[k])) : __uint_as_float(v[k]);
                 }
             }
             tc_fence_before();

@@ -819,19 +819,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 __syncwarp();
                 if (!ok) break;
                 tc_fence_after();
-                // column group j (4 latent columns) of all 128 rows is contiguous: 512 consecutive bytes a warp store
-                float4* oseg = reinterpret_cast<float4*>(p.o_part) +
-                               (out_row_base + static_cast<int64_t>(s.slot) * kRows) * (kDc / 4);
+                // the workspace holds [column / 32][row] x 32 fp32.  A thread has its row's 32 columns; four lanes exchange 8
+                // by 8 of them, so that they store a row's 128 bytes together
+                float* oseg = p.o_part + (out_row_base + static_cast<int64_t>(s.slot) * kRows) * kDc + (r & ~3) * 32 + 8 * (lane & 3);
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t v[32];
                     tmem_ld32(t_lane + 32 * c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        oseg[(32 * cq + 8 * c + k) * kRows + r] =
-                            make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
-                                        __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+                    for (int bit = 1; bit <= 2; bit *= 2)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (!(k & bit))
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    uint32_t &x = v[8 * k + e], &y = v[8 * (k | bit) + e];
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & bit) ? x : y, bit);
+                                    if (lane & bit) x = got;
+                                    else y = got;
+                                }
+                    // now v[8 k ..] is row (r & ~3) + k's, columns 8 (lane & 3) .. of the 32
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) st_global8(oseg + ((4 * cq + c) * kRows + k) * 32, v + 8 * k);
                 }
                 tc_fence_before();
                 mbar_arrive(&bars[kOBarOFree]);

@@ -82,23 +82,29 @@ int tc_clusters_per_group(int G, int num_splits, bool one_sm) {
     return pg < max_pairs_per_group(G) ? pg : max_pairs_per_group(G);
 }
 
-// Decode over the 8-bit cache: work units per group of 128 query rows, and the same workspace regions.  Units do not
-// wait on one another, so their number need not be what the device holds at once.
+// Decode over the 8-bit cache: work units per group of 128 query rows.  Units do not wait on one another, so their number
+// need not be what the device holds at once.
 bool one_sm8(int n_q, int H) { return static_cast<int64_t>(n_q) * H <= kMaxSm8Rows; }
 int units8(int n_q, int H) {
     return one_sm8(n_q, H) ? kMaxSmCtas : max_pairs_per_group((n_q * H + 127) / 128);
 }
 
-TcWs ws8_layout(int B, int n_q, int H) {
-    TcWs w;
+// Its workspace, from the first multiple of 32: segment partials [G][slots][rs rows] (R, l), then O as [G][slots] blocks
+// of [16 column groups of 32][rs rows] x 32 fp32.
+struct Ws8 {
+    int G, slots, rs;
+    size_t ml_part, o_part, total;
+};
+
+Ws8 ws8_layout(int B, int n_q, int H) {
+    Ws8 w;
     w.G = (n_q * H + 127) / 128;
     w.slots = B + units8(n_q, H);
     w.rs = one_sm8(n_q, H) ? (n_q * H <= 32 ? 32 : 64) : 128;
     const size_t rows = static_cast<size_t>(w.G) * w.slots * w.rs;
     w.ml_part = 0;
     w.o_part = align1k(rows * sizeof(float2));
-    w.olat = align1k(w.o_part + rows * kDc * sizeof(float));
-    w.total = w.olat + static_cast<size_t>(H) * olat_rows(B * n_q) * 1024;
+    w.total = w.o_part + rows * kDc * sizeof(float) + 16;
     return w;
 }
 
@@ -266,14 +272,13 @@ mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, co
     if (!q || !cache8 || !block_table || !kv_len || !W_UV || !out || !workspace) return MLA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(cache8) || !aligned16(W_UV) || !aligned16(out) || !aligned16(workspace))
         return MLA_ERR_INVALID_ARG;
-    const TcWs lay = ws8_layout(B, n_q, H);
+    const Ws8 lay = ws8_layout(B, n_q, H);
     if (ws_bytes < lay.total) return MLA_ERR_WORKSPACE;
     int units = units8(n_q, H);
     if (num_splits > 0 && num_splits < units) units = num_splits;
-    char* ws = static_cast<char*>(workspace);
+    char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
     float* o_part = reinterpret_cast<float*>(ws + lay.o_part);
     float2* ml_part = reinterpret_cast<float2*>(ws + lay.ml_part);
-    uint8_t* olat = reinterpret_cast<uint8_t*>(ws + lay.olat);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const uint16_t* qp = static_cast<const uint16_t*>(q);
     const uint8_t* cp = static_cast<const uint8_t*>(cache8);
@@ -283,11 +288,8 @@ mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, co
                         : launch_decode8_tc(qp, cp, cap_blocks, block_table, max_blocks, kv_len, B, n_q, H, scale, units,
                                             o_part, ml_part, lay.slots, dev_status, cs);
     if (e == cudaSuccess)
-        e = launch_merge(o_part, ml_part, kv_len, max_blocks, B, n_q, H, units, lay.slots, lay.rs, olat, lse_out,
-                         dev_status, cs, true);
-    if (e == cudaSuccess)
-        e = launch_upproj(olat, static_cast<const uint16_t*>(W_UV), B * n_q, H, static_cast<uint16_t*>(out), dev_status,
-                          cs);
+        e = launch_finish8(o_part, ml_part, kv_len, max_blocks, B, n_q, H, units, lay.slots, lay.rs,
+                           static_cast<const uint16_t*>(W_UV), static_cast<uint16_t*>(out), lse_out, dev_status, cs);
     return cuda_status(e);
 }
 

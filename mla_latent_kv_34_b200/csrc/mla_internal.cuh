@@ -135,6 +135,10 @@ cudaError_t launch_decode8_sm(const uint16_t* q, const uint8_t* cache, int64_t c
                               int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int ctas,
                               float* o_part, float2* ml_part, int slots, int rs, int32_t* dev_status,
                               cudaStream_t stream);
+// The merge of their pieces with the W^UV projection (finish8.cu).
+cudaError_t launch_finish8(const float* o_part, const float2* ml_part, const int32_t* kv_len, int max_blocks, int B, int n_q,
+                           int H, int P_g, int slots, int rs, const uint16_t* W_UV, uint16_t* out, float* lse_out,
+                           int32_t* dev_status, cudaStream_t stream);
 // Rows of the merged latent output o_lat kept for the up-projection: T rounded so that every 64-token
 // block but the last is full and the last is a multiple of 16 (the MMA N granularity).
 __host__ __device__ __forceinline__ int olat_rows(int T) {
@@ -143,8 +147,7 @@ __host__ __device__ __forceinline__ int olat_rows(int T) {
 }
 cudaError_t launch_merge(const float* o_part, const float2* ml_part, const int32_t* kv_len, int max_blocks, int B,
                          int n_q, int H, int P_g, int slots, int rs, uint8_t* olat, float* lse_out,
-                         int32_t* dev_status, cudaStream_t stream,
-                         bool nan_lse = false);  // nan_lse: a row whose sum is NaN gets lse = NaN, not -inf
+                         int32_t* dev_status, cudaStream_t stream);
 cudaError_t launch_upproj(const uint8_t* olat, const uint16_t* W_UV, int T, int H, uint16_t* out, int32_t* dev_status,
                           cudaStream_t stream);
 

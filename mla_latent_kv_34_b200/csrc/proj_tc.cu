@@ -261,7 +261,7 @@ template <int kSplit, int kVec>
 __global__ void __launch_bounds__(512) merge_kernel(
     const float* __restrict__ o_part, const float2* __restrict__ ml_part, const int32_t* __restrict__ kv_len,
     int max_blocks, int B, int n_q, int H, int P_g, int slots, int rs, uint8_t* __restrict__ olat,
-    float* __restrict__ lse_out, bool nan_lse) {
+    float* __restrict__ lse_out) {
     static_assert(kSplit >= 1 && kSplit <= 32 && (kSplit & (kSplit - 1)) == 0, "kSplit: power of two <= 32");
     static_assert(kVec == 2 || kVec == 4 || kVec == 8, "kVec: 2, 4 or 8 column groups");
     constexpr int kBatch = 8 / kVec;  // pieces whose loads are in flight together
@@ -384,8 +384,7 @@ __global__ void __launch_bounds__(512) merge_kernel(
         *reinterpret_cast<uint4*>(olat + olat_offset(T, h, t, col >> 6, (col & 63) >> 3)) = y;
     }
     if (slice == 0 && k == 0 && lse_out)
-        lse_out[static_cast<int64_t>(t) * H + h] =
-            (z > 0.f || (nan_lse && z != z)) ? (Mr + log2f(z)) * 0.69314718055994530942f : -CUDART_INF_F;
+        lse_out[static_cast<int64_t>(t) * H + h] = (z > 0.f) ? (Mr + log2f(z)) * 0.69314718055994530942f : -CUDART_INF_F;
 }
 
 // ------------------------------------------------------------------ up-projection
@@ -590,31 +589,31 @@ namespace proj {
 template <int kSplit, int kVec>
 cudaError_t launch_merge_t(int rows, dim3 grid, cudaStream_t stream, const float* o_part, const float2* ml_part,
                            const int32_t* kv_len, int max_blocks, int B, int n_q, int H, int P_g, int slots, int rs,
-                           uint8_t* olat, float* lse_out, bool nan_lse) {
+                           uint8_t* olat, float* lse_out) {
     grid.x = 128 / kVec;
     return launch_pdl(merge_kernel<kSplit, kVec>, grid, rows * kSplit, 0, stream, o_part, ml_part, kv_len,
-                      max_blocks, B, n_q, H, P_g, slots, rs, olat, lse_out, nan_lse);
+                      max_blocks, B, n_q, H, P_g, slots, rs, olat, lse_out);
 }
 
 template <int kSplit>
 cudaError_t launch_merge_s(int vec, int rows, dim3 grid, cudaStream_t stream, const float* o_part,
                            const float2* ml_part, const int32_t* kv_len, int max_blocks, int B, int n_q, int H,
-                           int P_g, int slots, int rs, uint8_t* olat, float* lse_out, bool nan_lse) {
+                           int P_g, int slots, int rs, uint8_t* olat, float* lse_out) {
     if (vec == 8)
         return launch_merge_t<kSplit, 8>(rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q, H, P_g,
-                                         slots, rs, olat, lse_out, nan_lse);
+                                         slots, rs, olat, lse_out);
     if (vec == 4)
         return launch_merge_t<kSplit, 4>(rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q, H, P_g,
-                                         slots, rs, olat, lse_out, nan_lse);
+                                         slots, rs, olat, lse_out);
     return launch_merge_t<kSplit, 2>(rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q, H, P_g, slots,
-                                     rs, olat, lse_out, nan_lse);
+                                     rs, olat, lse_out);
 }
 
 }  // namespace proj
 
 cudaError_t launch_merge(const float* o_part, const float2* ml_part, const int32_t* kv_len, int max_blocks, int B,
                          int n_q, int H, int P_g, int slots, int rs, uint8_t* olat, float* lse_out,
-                         int32_t* dev_status, cudaStream_t stream, bool nan_lse) {
+                         int32_t* dev_status, cudaStream_t stream) {
     (void)dev_status;
     if (B < 1 || rs < 1 || rs > 128 || (rs & 31) != 0) return cudaErrorInvalidValue;
     const int G = (n_q * H + 127) / 128;
@@ -630,15 +629,15 @@ cudaError_t launch_merge(const float* o_part, const float2* ml_part, const int32
     const dim3 grid(1, B, G);
     switch (split) {
         case 1: return proj::launch_merge_s<1>(vec, rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q,
-                                               H, P_g, slots, rs, olat, lse_out, nan_lse);
+                                               H, P_g, slots, rs, olat, lse_out);
         case 2: return proj::launch_merge_s<2>(vec, rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q,
-                                               H, P_g, slots, rs, olat, lse_out, nan_lse);
+                                               H, P_g, slots, rs, olat, lse_out);
         case 4: return proj::launch_merge_s<4>(vec, rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q,
-                                               H, P_g, slots, rs, olat, lse_out, nan_lse);
+                                               H, P_g, slots, rs, olat, lse_out);
         case 8: return proj::launch_merge_s<8>(vec, rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B, n_q,
-                                               H, P_g, slots, rs, olat, lse_out, nan_lse);
+                                               H, P_g, slots, rs, olat, lse_out);
         default: return proj::launch_merge_s<16>(vec, rows, grid, stream, o_part, ml_part, kv_len, max_blocks, B,
-                                                 n_q, H, P_g, slots, rs, olat, lse_out, nan_lse);
+                                                 n_q, H, P_g, slots, rs, olat, lse_out);
     }
 }
 

@@ -1,8 +1,9 @@
 """The 8-bit latent cache on the GPU: quantised append and read-back bit for bit, decode against 64 bits.
 
-Tolerances of decode8, from its roundings (u = 2^-8, half a bf16 step).  P is held by two terms within u of itself;
+Tolerances of decode8, from its roundings (u = 2^-8, half a bf16 step).  P is held by two terms within u of itself,
+or 2 u in the runs of 32 tokens where all are below the reference (their rounding is dithered);
 probabilities far below the largest lose more of themselves, but alike in both directions over the tokens, so that
-their sum keeps within another u of the whole.  With A = sum_t P_t |c_t| and d the error of
+their sum keeps within another u of the whole: 2 u in all.  With A = sum_t P_t |c_t| and d the error of
 a score (576 products summed in fp32: d <= 577 * 2^-23 * max_t sum |q_i c_ti| * scale), o_lat is off by at most
 (2 u + 2 d + 2^-14) A before its own rounding to bf16, and out is rounded once more:
     |out - ref| <= |W^UV| ((2 u + 2 d + 2^-14)(1 + u) A + u |o|) + u |ref| (1 + 2^-7) + 2^-20,
@@ -256,6 +257,57 @@ def test_decode8_against_64_bits(lengths, H, n_q):
     p.check(out, lse, l2=min(lengths) > 100)
 
 
+@pytest.mark.parametrize("lengths,H,n_q", [
+    ([1 + 7 * i % 300 for i in range(70)], 128, 1), ([3 + 11 * i % 170 for i in range(30)], 128, 3),
+    ([40 + 29 * i % 200 for i in range(9)], 5, 40), ([130, 7], 100, 1), ([1500, 700, 40], 40, 1),
+    ([1400, 9, 513], 24, 1), ([700, 900], 16, 3)])
+def test_decode8_many_rows_heads_and_pieces(lengths, H, n_q):
+    """Blocks of query rows of several sequences, several blocks a head, rows that straddle the
+    groups of 128, and one to three sequences a work unit."""
+    p = Problem8(lengths, H, n_q, seed=H)
+    out, lse = p.decode()
+    assert p.status.item() == 0
+    p.check(out, lse, l2=False)
+    p.check(*p.decode(num_splits=3), l2=False)
+
+
+def test_decode8_empty_sequences_between_others():
+    p = Problem8([1 + 5 * i % 130 for i in range(70)], 128, 1, seed=31)
+    gone = [0, 8, 9, 63, 64, 69]
+    kv = p.lengths.copy()
+    kv[gone] = 0
+    lse = torch.full((70, 128), 77.0, device="cuda")
+    out = mla.decode8(p.q, p.cache8, p.table, i32(kv), p.W, 1, SCALE, lse_out=lse, dev_status=p.status)
+    assert p.status.item() == 4
+    p.check(out, lse, seqs=[b for b in range(70) if b not in gone], l2=False)
+    assert (out[gone] == 0).all() and torch.isneginf(lse[gone]).all()
+
+
+def test_decode8_workspace_of_any_alignment_and_two_calls_at_once():
+    """Workspaces that start 16 bytes past a multiple of 32; calls on two streams that run at the same time."""
+    ps = [Problem8([500, 90], 128, 1, seed=40), Problem8([900, 64, 200], 16, 1, seed=41)]
+    ws = []
+    for p in ps:
+        n = mla.decode8_workspace_bytes(p.B, 1, p.H)
+        w = torch.full((n + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        at = 16 + (-w.data_ptr()) % 32
+        ws.append((w, at, w[at:at + n]))
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    res = []
+    for _ in range(3):
+        for p, (_w, _at, v), s in zip(ps, ws, streams):
+            lse = torch.empty(p.B, p.H, device="cuda")
+            with torch.cuda.stream(s):
+                out = mla.decode8(p.q, p.cache8, p.table, p.kv_len, p.W, 1, SCALE, workspace=v, lse_out=lse)
+            res.append((p, out, lse))
+    torch.cuda.synchronize()
+    for p, out, lse in res:
+        p.check(out, lse)
+    for (w, at, v) in ws:
+        assert (w[:at] == 0xFF).all() and (w[at + v.numel():] == 0xFF).all()
+
+
 def test_decode8_wide_range_of_scales():
     """Rows whose magnitudes differ by 2^20 within a tile: the large ones carry the output where they are."""
     p = Problem8([700, 300], 24, 1, seed=3, amp=4.0, q_amp=0.02, q=lambda q: 0.05 * q)
@@ -264,7 +316,7 @@ def test_decode8_wide_range_of_scales():
     p.check(*p.decode(), l2=False)
 
 
-@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("H", [16, 40, 128])
 @pytest.mark.parametrize("gap", [8.0, 12.0, 30.0])
 def test_decode8_sink_token(H, gap):
     """One token far above thousands of others, whose small P have to keep their sum: the first, and one in the middle."""
