@@ -298,12 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             bool ok = true;
             bool have = w.next(p, s);
             while (ok && have) {
-                wn = w;
-                const bool have_next = wn.next(p, sn);
-                const int t_pf = max(s.t0, s.t1 - 2);
-                const char* nq = (have_next && row_ok) ? reinterpret_cast<const char*>(
-                                                              p.q + (static_cast<int64_t>(sn.b) * p.R + rr) * kRow)
-                                                        : nullptr;
                 // this segment's query rows, two e4m3 terms each: latent columns 128 cq .. -> TMEM, RoPE columns 16 cq ..
                 // -> shared memory.  The warp loads its 32 rows coalesced (a lane per 16-byte unit) and transposes each
                 // 32-column chunk through a swizzled 2 KB tile into the lane-per-row order of tcgen05.st.  The bf16 rows
@@ -407,6 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars[kSBarQReady]);
+                // the next segment, whose queries are prefetched near the end of this one
+                wn = w;
+                const bool have_next = wn.next(p, sn);
+                const int t_pf = max(s.t0, s.t1 - 2);
+                const char* nq = (have_next && row_ok) ? reinterpret_cast<const char*>(
+                                                              p.q + (static_cast<int64_t>(sn.b) * p.R + rr) * kRow)
+                                                        : nullptr;
                 // from here on a thread has rows rA = 32 qd + lane % 16 and rB = rA + 16, and 16 of the warp's columns: the
                 // tokens' scales are then read and unpacked once for two rows
                 const float rowfA = __shfl_sync(0xffffffffu, rowf, lane & 15), rowfB = __shfl_sync(0xffffffffu, rowf, 16 + (lane & 15));
