@@ -232,40 +232,52 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 while (ok && w.next(p, s)) {
                     ok = mbar_wait(&bars[kSBarQReady], kseg & 1u, abort_flag, kLimitNs);
                     ++kseg;
+                    bool ready = false;  // the tile and its score buffer were seen to be there while the last one's MMAs went out
                     for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                         const uint32_t sb = n & 1u, us = n >> 1;
-                        ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
+                        if (!ready)
+                            ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs) &&
+                                 mbar_wait(&bars[kSBarFull + 2 * sb], us & 1u, abort_flag, kLimitNs);
+                        if (!ok) break;
+                        tc_fence_after();
                         const uint32_t d = tmem + col_s(sb);
                         const uint64_t tile_off = static_cast<uint64_t>(sb * kTileBytes) >> 4;
+                        bool next = false;
+                        // rolled: code that fits the instruction cache beside the softmax warps' (fully unrolled, the issue of
+                        // a tile's 36 MMAs took longer than their 2304 cycles)
 #pragma unroll 1
-                        for (int k = 0; ok && k < 2; ++k) {
-                            ok = mbar_wait(&bars[kSBarFull + 2 * sb + k], us & 1u, abort_flag, kLimitNs);
-                            if (!ok) break;
-                            tc_fence_after();
-                            // rolled: code that fits the instruction cache beside the softmax warps' (fully unrolled, the
-                            // issue of a tile's 36 MMAs took longer than their 2304 cycles)
-#pragma unroll 1
-                            for (int j = 0; j < 2; ++j) {
-                                const int c = 2 * k + j;
-                                const uint64_t cd = ring_desc + tile_off + (static_cast<uint64_t>(c * kChunk) >> 4);
-                                const uint32_t qa = tmem + kColQ + 32 * c;
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    mma8_ts(d, qa + 8 * kk, cd + 2 * kk, idesc, (c | kk) ? 1u : 0u);
-                                    mma8_ts(d, qa + 128 + 8 * kk, cd + 2 * kk, idesc, 1u);
-                                }
+                        for (int c = 0; c < 4; ++c) {
+                            if (c == 2 && !ready) {
+                                ok = mbar_wait(&bars[kSBarFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
+                                if (!ok) break;
+                                tc_fence_after();
                             }
-                            if (k == 1) {
-                                const uint64_t rd = rope_desc + tile_off;
-#pragma unroll
-                                for (int kk = 0; kk < 2; ++kk) {
-                                    mma8_ss(d, qr_desc + 2 * kk, rd + 2 * kk, idesc, 1u);
-                                    mma8_ss(d, qr_desc + 4 + 2 * kk, rd + 2 * kk, idesc, 1u);
-                                }
+                            // asked for while MMAs are still queued, so that the next tile's follow at once
+                            if (c == 3 && t + 1 < s.t1) {
+                                const uint32_t un = (n + 1) >> 1;
+                                next = mbar_poll(smem_u32(&bars[kSBarSEmpty + (sb ^ 1u)]), (un & 1u) ^ 1u) &&
+                                       mbar_poll(smem_u32(&bars[kSBarFull + 2 * (sb ^ 1u)]), un & 1u) &&
+                                       mbar_poll(smem_u32(&bars[kSBarFull + 2 * (sb ^ 1u) + 1]), un & 1u);
                             }
-                            mma_commit(smem_u32(&bars[kSBarEmpty + 2 * sb + k]));
+                            const uint64_t cd = ring_desc + tile_off + (static_cast<uint64_t>(c * kChunk) >> 4);
+                            const uint32_t qa = tmem + kColQ + 32 * c;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                mma8_ts(d, qa + 8 * kk, cd + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+                                mma8_ts(d, qa + 128 + 8 * kk, cd + 2 * kk, idesc, 1u);
+                            }
+                            if (c == 1) mma_commit(smem_u32(&bars[kSBarEmpty + 2 * sb]));
                         }
-                        if (ok) mma_commit(smem_u32(&bars[kSBarSFull + sb]));
+                        if (!ok) break;
+                        const uint64_t rd = rope_desc + tile_off;
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            mma8_ss(d, qr_desc + 2 * kk, rd + 2 * kk, idesc, 1u);
+                            mma8_ss(d, qr_desc + 4 + 2 * kk, rd + 2 * kk, idesc, 1u);
+                        }
+                        mma_commit(smem_u32(&bars[kSBarSFull + sb]));
+                        mma_commit(smem_u32(&bars[kSBarEmpty + 2 * sb + 1]));
+                        ready = next;
                     }
                 }
                 if (!ok) raise_abort(abort_flag, peer_abort, p.dev_status);
