@@ -124,13 +124,6 @@ __device__ __forceinline__ void find_first(const Params& p, int pidx, int lane, 
     }
 }
 
-// Largest magnitude bits of two packed bf16 into the running packed maximum.
-__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b32 a;\n\tand.b32 a, %2, 0x7fff7fff;\n\tmax.u16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
-    return r;
-}
-
 // Exponent a of a query row whose largest magnitude has bf16 bits `top`: 2^a is the least power of two (>= 2^-120)
 // with largest <= 448 * 2^a.  0 for a row of zeros.
 __device__ __forceinline__ int row_exp(uint32_t top) {

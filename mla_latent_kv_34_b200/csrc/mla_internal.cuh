@@ -45,11 +45,6 @@ __host__ __device__ __forceinline__ int block_offset(int r, int c) {
     return (c >> 6) * kBlockChunk + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
 }
 
-// Byte offset of column c of row r inside a block of the 8-bit cache.
-__host__ __device__ __forceinline__ int block8_offset(int r, int c) {
-    return c < kDc ? (c >> 7) * kBlock8Chunk + r * 128 + ((((c & 127) >> 4) ^ (r & 7)) << 4) + (c & 15)
-                   : kBlock8Rope + r * 64 + ((((c - kDc) >> 4) ^ ((r >> 1) & 3)) << 4) + (c & 15);
-}
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
     return __uint_as_float(static_cast<uint32_t>(b) << 16);

@@ -213,6 +213,13 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// Largest magnitude bits of two packed bf16 into the running packed maximum.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 a;\n\tand.b32 a, %2, 0x7fff7fff;\n\tmax.u16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+    return r;
+}
+
 // 32 consecutive bytes (32-byte aligned).
 __device__ __forceinline__ void st_global8(float* p, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),

@@ -130,11 +130,12 @@ def special_rows(n, rng):
     return f32_to_bf16_bits(x), f32_to_bf16_bits(k)
 
 
-@pytest.mark.parametrize("T", [1, 2, 7, 129, 700])
+@pytest.mark.parametrize("T", [1, 2, 7, 129, 700, 9601])
 def test_append8_bit_exact(T):
     rng = np.random.default_rng(T)
     c, k = special_rows(T, rng)
-    mb, cap, nseq = 6, 30, 4
+    mb, nseq = (7, 4) if T <= 700 else (25, 4)
+    cap = nseq * mb + 2
     tables = rng.permutation(cap)[:nseq * mb].reshape(nseq, mb).astype(np.int32)
     place = rng.permutation(nseq * mb * 128)[:T]
     seq, pos = (place // (mb * 128)).astype(np.int32), (place % (mb * 128)).astype(np.int32)
