@@ -2,11 +2,12 @@
 //
 //   o[t, h] = sum_p 2^(R_p - M) O_p / sum_p 2^(R_p - M) l_p    over the pieces p of t's sequence, M = max_p R_p
 //   lse     = (M + log2 sum_p 2^(R_p - M) l_p) ln 2            (R_p integers: exact factors)
-//   out[t, h, :] = W^UV_h bf16(o[t, h])                        (128 = 128 x 512)
+//   out[t, h, :] = W^UV_h o[t, h]                              (128 = 128 x 512)
 //
 // One CTA per (block of query rows, head): its 16 warps merge the rows, each a row at a time (or, with fewer rows than
 // warps, several warps a row, each over a part of the pieces), into shared memory as the B operand of 32 MMAs
-// (M = 128 output columns, N = rows, K = 512) whose A operand, W^UV_h, is under way by TMA before the attend kernel ends.
+// (M = 128 output columns, N = 2 rows, K = 512: o as bf16 and what that leaves as a second bf16 row, whose results are added;
+// o rounded once was the call's largest error, 0.0017 of 0.0027 in the 2-norm) whose A operand, W^UV_h, is under way by TMA before the attend kernel ends.
 // It has to move the pieces (2 KB a row and piece, from L2) and W^UV_h (128 KB a CTA, from HBM once), 4 us at B 32, H 128;
 // what it takes, 8 to 13 us after the attend kernel, is latency: lengths, pieces, sums, MMAs, result, one after the other.
 // A warp therefore keeps four pieces' loads in flight, of whichever rows, and what depends on the lengths alone is done
@@ -32,18 +33,18 @@ namespace fin8 {
 using namespace d8;
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kMaxRows = 64;
+constexpr int kMaxRows = 32;
 constexpr int kSms = 148;
 constexpr int kBatch = 4;  // pieces whose loads are in flight together (64 bytes a lane each)
 constexpr int kWBytes = kDh * kDc * 2, kWChunk = kDh * 128;
 constexpr int kOffPart = kWBytes;                        // [16 warps][4][32 lanes] float4: a warp's share of a row; then out
 constexpr int kOffMz = kOffPart + kWarps * 2048;         // [16 warps] (M, z)
-constexpr int kOffTab = kOffMz + kWarps * 8;             // [64] the block's rows: Row
-constexpr int kOffSeq = kOffTab + kMaxRows * 16;         // [64] tiles of the block's sequences; pieces (first, how many)
+constexpr int kOffTab = kOffMz + kWarps * 8;             // [32] the block's rows: Row
+constexpr int kOffSeq = kOffTab + kMaxRows * 16;         // [32] tiles of the block's sequences; pieces (first, how many)
 constexpr int kOffBar = kOffSeq + kMaxRows * 8;          // W there, MMAs done
 constexpr int kOffRed = kOffBar + 16;                    // [2][16] tile counts; TMEM address
-constexpr int kOffO = ((kOffRed + 2 * kWarps * 4 + 16 + 1023) / 1024) * 1024;  // o: 8 chunks of [N rows x 64 columns] bf16, swizzled
-static_assert(kOffO + kMaxRows * 1024 <= 232448 && kMaxRows * kDh * 2 <= kOffMz - kOffPart, "shared memory");
+constexpr int kOffO = ((kOffRed + 2 * kWarps * 4 + 16 + 1023) / 1024) * 1024;  // o: 8 chunks of [N rows x 64 columns] bf16, swizzled; rows, then their second terms
+static_assert(kOffO + 2 * kMaxRows * 1024 <= 232448 && kMaxRows * kDh * 2 <= kOffMz - kOffPart, "shared memory");
 static_assert(kOffTab % 16 == 0 && kOffBar % 8 == 0, "alignment");
 
 struct Row {
@@ -58,7 +59,7 @@ struct FinParams {
     uint16_t* out;
     float* lse;
     int32_t* dev_status;
-    int max_blocks, B, n_q, H, P_g, slots, rs, rows;  // rows: query rows a CTA (8, 16, 32 or 64)
+    int max_blocks, B, n_q, H, P_g, slots, rs, rows;  // rows: query rows a block (8, 16 or 32)
 };
 
 __device__ __forceinline__ void ld_global8(const float* p, float* v) {
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffRed + 2 * kWarps * 4);
     const int h = blockIdx.y;
     const int T = p.B * p.n_q;
-    const int N = max(16, p.rows);  // B operand rows (those past n are not written, nor their results read)
+    const int N = 2 * p.rows;  // B operand rows (those past n are not written, nor their results read)
     volatile int never = 0;
     if ((sbase & 1023u) != 0) {
         if (tid == 0) report(p.dev_status, MLA_DEVERR_TIMEOUT);
@@ -93,43 +94,41 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
         for (int c = 0; c < 8; ++c) tma_load_3d(sbase + c * kWChunk, &wmap, 0, h * kDh, c, &bars[0]);
     }
     if (warp == 0) tmem_alloc(tmem_slot, 64);
+    // tiles of all sequences, and of those before the first block's first (the lengths are inputs too)
+    int b_at = blockIdx.x * p.rows / p.n_q, s_all = 0, s_pre = 0;
+    for (int i = tid; i < p.B; i += kThreads) {
+        const int tiles = valid_seq_tiles(p.kv_len[i], p.n_q, p.max_blocks);
+        s_all += tiles;
+        if (i < b_at) s_pre += tiles;
+    }
+    s_all = __reduce_add_sync(0xffffffffu, s_all);
+    s_pre = __reduce_add_sync(0xffffffffu, s_pre);
+    if (lane == 0) {
+        red[warp] = s_all;
+        red[kWarps + warp] = s_pre;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    int Nt = 0, pre = 0;  // pre: tiles of the sequences before b_at
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        Nt += red[w];
+        pre += red[kWarps + w];
+    }
     bool ok = true;
     for (uint32_t it = 0, t0 = blockIdx.x * p.rows; ok && t0 < T; ++it, t0 += gridDim.x * p.rows) {
         const int n = min(p.rows, T - t0);
-        // tiles of all sequences, of those before the block's first, and of the block's own (the lengths are inputs too)
-        const int b0 = t0 / p.n_q, nb = (t0 + n - 1) / p.n_q - b0 + 1;
-        int s_all = 0, s_pre = 0;
-        for (int i = tid; i < p.B; i += kThreads) {
-            const int tiles = valid_seq_tiles(p.kv_len[i], p.n_q, p.max_blocks);
-            s_all += tiles;
-            if (i < b0) s_pre += tiles;
-            else if (i < b0 + nb) seq[i - b0].x = tiles;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            s_all += __shfl_xor_sync(0xffffffffu, s_all, o);
-            s_pre += __shfl_xor_sync(0xffffffffu, s_pre, o);
-        }
-        if (lane == 0) {
-            red[warp] = s_all;
-            red[kWarps + warp] = s_pre;
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        int Nt = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) Nt += red[w];
         if (warp == 0) {
-            int pre = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) pre += red[kWarps + w];
-            const int a = 2 * lane < nb ? seq[2 * lane].x : 0, c = 2 * lane + 1 < nb ? seq[2 * lane + 1].x : 0;
-            int inc = a + c;
+            // the block's sequences b0 .. b0 + nb - 1 and rows
+            const int b0 = t0 / p.n_q, nb = (t0 + n - 1) / p.n_q - b0 + 1;
+            int more = 0;
+            for (int i = b_at + lane; i < b0; i += 32) more += valid_seq_tiles(p.kv_len[i], p.n_q, p.max_blocks);
+            pre += __reduce_add_sync(0xffffffffu, more);
+            b_at = b0;
+            const int nt = lane < nb ? valid_seq_tiles(p.kv_len[b0 + lane], p.n_q, p.max_blocks) : 0;
+            int inc = nt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -138,21 +137,17 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
             // a sequence's pieces: the work units whose tile range meets its own, [ts, ts + tiles).  With at least as many
             // tiles as units they follow one another: (the first, how many); otherwise a unit has one tile or none, and
             // each tile is a piece: (its first tile, how many)
-            const int64_t P = p.P_g;
-            const int ts[2] = {pre + inc - a - c, pre + inc - c}, nt[2] = {a, c};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                int2 e = make_int2(ts[i], nt[i]);
-                if (Nt >= p.P_g && nt[i] > 0) {
-                    e.x = static_cast<int>(((ts[i] + 1) * P - 1) / Nt);
-                    e.y = static_cast<int>(((ts[i] + nt[i]) * P - 1) / Nt) - e.x + 1;
-                }
-                seq[2 * lane + i] = e;
+            const int64_t ts = pre + inc - nt, P = p.P_g;
+            int2 e = make_int2(static_cast<int>(ts), nt);
+            if (Nt >= p.P_g && nt > 0) {
+                e.x = static_cast<int>(((ts + 1) * P - 1) / Nt);
+                e.y = static_cast<int>(((ts + nt) * P - 1) / Nt) - e.x + 1;
             }
+            seq[lane] = e;
             __syncwarp();
-            for (int i = lane; i < n; i += 32) {
-                const int b = (t0 + i) / p.n_q, rr = (t0 + i - b * p.n_q) * p.H + h;
-                tab[i] = {seq[b - b0].x, seq[b - b0].y, (rr >> 7) * p.slots + b, rr & 127};
+            if (lane < n) {
+                const int b = (t0 + lane) / p.n_q, rr = (t0 + lane - b * p.n_q) * p.H + h;
+                tab[lane] = {seq[b - b0].x, seq[b - b0].y, (rr >> 7) * p.slots + b, rr & 127};
             }
         }
         __syncthreads();
@@ -171,12 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int j = lane + 32 * q;  // columns 8 j .. 8 j + 7
-                uint4 y;
-                y.x = pack_bf16x2(acc[4 * q].x * inv, acc[4 * q].y * inv);
-                y.y = pack_bf16x2(acc[4 * q + 1].x * inv, acc[4 * q + 1].y * inv);
-                y.z = pack_bf16x2(acc[4 * q + 2].x * inv, acc[4 * q + 2].y * inv);
-                y.w = pack_bf16x2(acc[4 * q + 3].x * inv, acc[4 * q + 3].y * inv);
-                *reinterpret_cast<uint4*>(smem + kOffO + (j >> 3) * N * 128 + i * 128 + (((j & 7) ^ (i & 7)) << 4)) = y;
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float a = acc[4 * q + w].x * inv, b = acc[4 * q + w].y * inv;
+                    hi[w] = pack_bf16x2(a, b);
+                    lo[w] = pack_bf16x2(a - __uint_as_float(hi[w] << 16), b - __uint_as_float(hi[w] & 0xFFFF0000u));
+                }
+                uint8_t* at = smem + kOffO + (j >> 3) * N * 128 + i * 128 + (((j & 7) ^ (i & 7)) << 4);
+                *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(at + p.rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             if (lane == 0 && p.lse)  // nothing visible: -inf; a NaN shows
                 p.lse[static_cast<int64_t>(t0 + i) * p.H + h] =
@@ -292,14 +291,17 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
         if (ok) {
             // lane = output column; row j's 128 are staged as 256 bytes
             const int d = 32 * (warp & 3) + lane;
-            for (int j0 = 8 * (warp >> 2); j0 < n; j0 += 32) {
-                uint32_t v[8];
-                tmem_ld8(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + j0, v);
+            const int j0 = 8 * (warp >> 2);
+            if (j0 < n) {
+                uint32_t v[8], w[8];
+                const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + j0;
+                tmem_ld8(at, v);
+                tmem_ld8(at + p.rows, w);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     *reinterpret_cast<uint16_t*>(smem + kOffPart + (j0 + j) * (kDh * 2) + 2 * d) =
-                        f32_to_bf16_rne(__uint_as_float(v[j]));
+                        f32_to_bf16_rne(__uint_as_float(v[j]) + __uint_as_float(w[j]));
             }
         }
         tc_fence_before();
@@ -330,9 +332,9 @@ cudaError_t launch_finish8(const float* o_part, const float2* ml_part, const int
     while (rows < fin8::kMaxRows && static_cast<int64_t>(H) * ((T + rows - 1) / rows) > fin8::kSms) rows *= 2;
     const int blocks = (T + rows - 1) / rows;
     const fin8::FinParams prm = {o_part, ml_part, kv_len, out, lse_out, dev_status, max_blocks, B, n_q, H, P_g, slots, rs, rows};
-    const int smem = fin8::kOffO + std::max(16, rows) * 1024;
+    const int smem = fin8::kOffO + 2 * rows * 1024;
     cudaError_t e = cudaFuncSetAttribute(fin8::finish8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         fin8::kOffO + fin8::kMaxRows * 1024);
+                                         fin8::kOffO + 2 * fin8::kMaxRows * 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(blocks, fin8::kSms / H), H);
