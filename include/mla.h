@@ -271,10 +271,14 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
  * place of the bf16 rows.  Arguments, shapes, results and errors are those of
  * mla_decode, but for
  *   cache8     pool of cap_blocks blocks of MLA_BLOCK8_BYTES, written by
- *              mla_append_cache8 (bytes of no token are never used)
+ *              mla_append_cache8 (a token's scale has to be a power of two;
+ *              bytes of no token are never used)
  *   workspace  of at least mla_decode8_workspace_bytes() bytes
- * The query stays bf16 and scores are formed from it and the codes without a
- * further rounding of either; sums, softmax and scales are fp32.
+ * Scores are formed from the bf16 query and the codes without a further
+ * rounding of either (query elements below 2^-10 of their row's largest are
+ * held to 2^-19 of it); sums, softmax and scales are fp32.  A NaN among a
+ * row's visible tokens, or a NaN or infinity in its query, makes its out and
+ * lse NaN.
  */
 size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits);
 mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks,

@@ -3,9 +3,9 @@
 //
 // Two terms.  The tensor cores multiply 8-bit values, so the codes of the cache go into them as they stand.  The other
 // operand, a bf16 query or an fp32 probability, is written as hi + lo: hi (e4m3) holds 4 significant bits, lo what is
-// left.  For the query lo is e4m3 too, the next 4 bits: a bf16 value (8 significant bits) is represented exactly as long as its last bit is at
-// least 2^-9 (the e4m3 step near 0); scaled by a power of two so that the row's largest value lies in (224, 448], that
-// is every element down to 2^-10 of the largest, and an absolute 2^-19 of the largest below.
+// left.  For the query lo is e4m3 too, the next 4 bits: a bf16 value (8 significant bits) is held exactly as long as its
+// last bit is at least 2^-9 (the e4m3 step near 0); scaled by a power of two so that the row's largest value lies in
+// (224, 448], that is every element down to 2^-10 of the largest, and an absolute 2^-19 of the largest below.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -188,11 +188,13 @@ __device__ __forceinline__ uint32_t round_term(uint32_t mask, uint32_t dither, u
 // e5m2's 3 significant bits: e5m2 is the upper half of an fp16, so an integer addition to the lower byte rounds it.  Down
 // to p = 2^-6 the pair holds p within 2^-8, like a bf16.  Below, hi's steps are 2^-9 and lo goes on to 2^-16, and many
 // equal small probabilities (a long tail behind one dominant token) would move their sum by up to an eighth if each were
-// rounded to nearest.  So where all of a row's probabilities in a unit are below 1 (`mask`; the reference is another
-// unit's), lo's rounding is dithered, over the tokens alike, which keeps the sum; where one is above, its unit's tail is
-// too small beside it to matter.
-__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t mask, uint32_t dither01,
-                                         uint32_t dither23, uint32_t& hi, uint32_t& lo) {
+// rounded to nearest.  So where all of a row's probabilities in a unit of tokens are far below 1 (`mask`; the reference is
+// another unit's), lo's rounding is dithered over the tokens, which keeps the sum, at twice the error of each (2^-7).  Where
+// one is larger, its unit's tail cannot move the unit's sum by more than 2^-8: 31 times 2^-17 against 2^-4 in the pair
+// kernel's units, 127 times against 2^-2 in whole tiles.  (Dithered from 1 down, the error of a call was 0.0025 instead of
+// 0.0021; chosen by element, the attend phase took 92 us instead of 86.)
+__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t mask01, uint32_t mask23,
+                                         uint32_t dither01, uint32_t dither23, uint32_t& hi, uint32_t& lo) {
     uint32_t h01, h23, d01, d23;
     uint16_t a, b;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
@@ -202,13 +204,13 @@ __device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3,
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d01) : "r"(h01), "r"(e4m3x2_to_f16x2(a)));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
     hi = a | (static_cast<uint32_t>(b) << 16);
-    lo = __byte_perm(d01 + round_term(mask, dither01, 0x00800080u), d23 + round_term(mask, dither23, 0x00800080u), 0x7531);
+    lo = __byte_perm(d01 + round_term(mask01, dither01, 0x00800080u), d23 + round_term(mask23, dither23, 0x00800080u), 0x7531);
 }
 // The same with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant bits down
-// to 2^-10 and steps of 2^-13 below, dithered alike (`add01`, `add23`: what to add before the last seven bits are cut off).  An e4m3 code of x has the bits
-// of the fp16 of 2^-8 x, less its top exponent bit and its last seven.
-__device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t add01, uint32_t add23,
-                                           uint32_t& hi, uint32_t& lo) {
+// to 2^-10 and steps of 2^-13 below.  With the one bit more, a dithered rounding (`dither`: seven bits for each half) of
+// every probability still holds it within 2^-8.  An e4m3 code of x has the bits of the fp16 of 2^-8 x, less its top exponent bit and its last seven.
+__device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t dither, uint32_t& hi,
+                                           uint32_t& lo) {
     uint32_t h01, h23, d01, d23;
     uint16_t a, b;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
@@ -219,8 +221,8 @@ __device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d01) : "r"(0x2C002C00u));  // 2^-4
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d23) : "r"(0x2C002C00u));
-    d01 += add01;
-    d23 += add23;
+    d01 += dither;
+    d23 += dither;
     hi = a | (static_cast<uint32_t>(b) << 16);
     lo = __byte_perm(((d01 << 1) & 0x7F007F00u) | (d01 & 0x80008000u), ((d23 << 1) & 0x7F007F00u) | (d23 & 0x80008000u), 0x7531);
 }
@@ -233,8 +235,9 @@ __host__ __device__ constexpr uint32_t dither_pair(int k) {
 
 // The reference exponent of a row's probabilities, P' = 2^(y - R) with y = log2(p s_t) (s_t, the token's scale, is
 // folded into P because V's rows are codes).  O and the sum are kept relative to R, an integer, so moving it multiplies
-// them by an exact power of two.  P' has to stay below 448 (e4m3): R moves up when a unit's largest y - R exceeds 8.75, and then (as at a piece's first tile) to where the largest P' lies in (1, 2].  It need not move down: a probability
-// 2^-20 of the largest is still held by split4_p, and 2^17 tokens below that are less than 1/8 of the sum.
+// them by an exact power of two.  P' has to stay below 448 (e4m3): R moves up when a unit's largest y - R exceeds 8.75, and
+// then (as at a piece's first tile) to where the largest P' lies in (1, 2].  It need not move down: a probability 2^-20 of
+// the largest is still held by the two terms, and 2^17 tokens below that are less than 1/8 of the sum.
 struct RowRef {
     float R;
     __device__ __forceinline__ void reset() { R = __uint_as_float(0xFF800000u); }
@@ -255,8 +258,8 @@ struct RowRef {
         return from == __uint_as_float(0xFF800000u) ? 1.f : factor(static_cast<int>(fmaxf(from - to, -127.f)));
     }
     __device__ __forceinline__ float minus() const { return R == __uint_as_float(0xFF800000u) ? 0.f : -R; }
-    // All ones where a unit's probabilities are all below 1 (round_term's mask).
-    __device__ __forceinline__ uint32_t low(float top) const { return top < R ? 0xFFFFFFFFu : 0u; }
+    // All ones where a unit's probabilities are all below 2^-k (round_term's mask).
+    __device__ __forceinline__ uint32_t low(float top, float k) const { return top < R - k ? 0xFFFFFFFFu : 0u; }
 };
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 operands (a_e5m2, b_e5m2: that one e5m2) and fp32 D.

@@ -7,9 +7,11 @@
 //                                           columns of their own, added at the end), or, where those do not fit, 32 of
 //                                           N = NR (lo as e5m2)
 // (NR: the rows rounded up to 16, 32 or 48).  Scores and O^T fit one SM's tensor memory, so a block is read once, by one
-// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token, 1.67 us a block and SM with all SMs reading; the
-// MMAs of a block take about half of that, and a ring of two blocks keeps the reads going (the bf16 kernel's ring holds
-// one, and its reads wait for its MMAs).
+// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token.  B 64, H 16, 4K: 41 us for the attend phase, 24 at a
+// copy's rate; once under way a tile takes 3600 cycles an SM (5.6 TB/s), the rest is the start (5500 cycles to the first
+// copy, then all SMs' first tiles at once) and the end (scores, softmax, aggregation and output of the last tile, 7000).
+// A ring of 2.75 tiles instead of two changed that by 2 %.  Waiting for the next tile's copies before the aggregation at hand
+// is issued, and a lo term with MMAs of its own, took 62 us.
 //
 // Softmax: a thread per token (tensor-memory lane) and half the rows; a set of four warps has a tile's 128 tokens.  A row's
 // maximum over a warp's tokens is a warp reduction, then the set's warps exchange them at one barrier and each decides on
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     for (int i = 0; i < RN; ++i) lp[i] *= RowRef::factor(__shfl_sync(0xffffffffu, d, i));
                 }
                 if (lane < RN) refs[lane] = ref.R;
-                const uint32_t lows = __ballot_sync(0xffffffffu, ref.low(top) != 0);
+                const uint32_t lows = L::kStack ? 0u : __ballot_sync(0xffffffffu, ref.low(top, 2.f) != 0);
                 __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
@@ -455,15 +457,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                         v[k] = ex2_approx(Rs[k] == -CUDART_INF_F ? (y[i + k] != y[i + k] ? y[i + k] : -CUDART_INF_F) : y[i + k] - Rs[k]);
                         lp[i + k] = fmaf(v[k], inv_s, lp[i + k]);
                     }
-                    // (the four are one token's in four rows: the masks differ within a pair)
-                    uint32_t add[2];
+                    if (L::kStack) {
+                        split4_p16(v[0], v[1], v[2], v[3], (dither >> 1) & 0x007F007Fu, hi[i / 4], lo[i / 4]);
+                    } else {
+                        // (the four are one token's in four rows: the masks differ within a pair)
+                        uint32_t mask[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t mask = ((lows >> (i + 2 * k)) & 1u ? 0x0000FFFFu : 0u) | ((lows >> (i + 2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
-                        add[k] = L::kStack ? round_term(mask, (dither >> 1) & 0x007F007Fu, 0x00400040u) : round_term(mask, dither, 0x00800080u);
+                        for (int k = 0; k < 2; ++k)
+                            mask[k] = ((lows >> (i + 2 * k)) & 1u ? 0x0000FFFFu : 0u) | ((lows >> (i + 2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+                        split4_p(v[0], v[1], v[2], v[3], mask[0], mask[1], dither, dither, hi[i / 4], lo[i / 4]);
                     }
-                    if (L::kStack) split4_p16(v[0], v[1], v[2], v[3], add[0], add[1], hi[i / 4], lo[i / 4]);
-                    else split4_p(v[0], v[1], v[2], v[3], 0xFFFFFFFFu, add[0], add[1], hi[i / 4], lo[i / 4]);
                 }
                 ok = mbar_wait(&bars[kBPFree + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
                 // row r, token tk: byte tk % 16 of the 16-byte unit tk / 16, at (unit ^ (row % 8)) of its 128-byte row

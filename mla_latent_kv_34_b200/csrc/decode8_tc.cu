@@ -1,19 +1,31 @@
-// Absorbed MLA decode over the 8-bit cache on the tensor cores (tcgen05 + TMEM), more than 32 query rows.
+// Absorbed MLA decode over the 8-bit cache on the tensor cores (tcgen05 + TMEM), more than 48 query rows.
 //
 // The step is mla_decode's (decode_tc.cu): a cluster of two CTAs owns 128 query rows, the "S" CTA forms the scores and
 // the softmax, the "O" CTA keeps O[128 x 512] in its whole tensor memory and accumulates P V; the (sequence, tile)
-// space is cut into equal ranges, one per cluster, and a range's pieces of sequences go to the workspace for the merge.
-// What differs is that a cached row is c_t = s_t code_t with e4m3 codes:
+// space is cut into equal ranges, one per cluster, and a range's pieces of sequences go to the workspace for the merge
+// (finish8.cu).  What differs is that a cached row is c_t = s_t code_t with e4m3 codes:
 //   - the codes are the operands of both contractions as they lie in the block (kind::f8f6f4, K = 32): no
-//     dequantisation, half the bytes from HBM and through shared memory.  Q and P are written as hi + lo of two e4m3
-//     terms (decode8_common.cuh), so Q is exact and P keeps 8 significant bits; two K = 32 MMAs at twice the bf16 rate
+//     dequantisation, half the bytes from HBM and through shared memory.  Q and P are written as hi + lo terms
+//     (decode8_common.cuh), so Q is exact and P keeps 8 significant bits; two K = 32 MMAs at twice the bf16 rate
 //     cost what the bf16 MMA of the same elements costs;
-//   - scores: x = S * (2^a scale log2 e) * s_t with the query row's power of two 2^a; P' = 2^(x + log2 s_t - R) carries
+//   - scores: y = S s_t (2^a scale log2 e) + log2 s_t with the query row's power of two 2^a; P' = 2^(y - R) carries
 //     s_t, because the rows of V are codes, and the row's sum takes P' / s_t.  R is RowRef's reference exponent;
 //   - a tile (72 KB of codes) comes as copies of 32 and 40 KB into a ring that holds two tiles, so a tile's copies are
 //     under way while the one before it is multiplied.
 // S CTA: the query's latent part in TMEM (hi 128 columns, lo 128 columns), its RoPE part in shared memory, two score
-// buffers of 128 columns; 36 MMAs (M = 128, N = 128) a tile.  O CTA: 16 MMAs (M = 128, N = 256) a tile.
+// buffers of 128 columns; 36 MMAs (M = 128, N = 128) a tile.  O CTA: 16 MMAs (M = 128, N = 256) a tile, P from shared memory.
+//
+// Softmax: sixteen warps, (quadrant of 32 rows) x (quarter tile of 32 tokens); a thread has two rows and 16 tokens, so the
+// tokens' scales are unpacked once for two rows.  The four units of a row in a tile follow one another only in R, which a
+// warp hands to the next as soon as its maximum is known; nothing else holds the warps in step.  P goes out in messages of
+// two units: staged in shared memory, one bulk copy to the O CTA's slot, whose barrier the O CTA arms itself.
+//
+// What bounds it: a tile takes about 3100 cycles; its score MMAs 2304, the S CTA's shared memory 2750 (MMA operands, copies
+// in and out, P, scales), a softmax warp's own instructions 2700.  At B 32, H 128, 8K the attend phase takes 86 to 92 us
+// (45 at the bf16 rate), of which 12 are the start (queries to codes, first tile) and as many a second sequence's start;
+// 4 x 128K 135 to 141 (89), ragged 128 x 2 tokens of 1 to 32K 1.0 ms (736 us), 1.2 ms under the power limit.  A first form
+// on CUDA cores took 7.3, 14.6 and 89 ms.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 ->
+// 93.9 us), all of a query's loads before the first is used (more registers and code: 91 -> 96 us).
 //
 // Every wait is bounded: on expiry the kernel records MLA_DEVERR_TIMEOUT, both CTAs of the pair abandon their loops,
 // let in-flight copies and MMAs land, free TMEM and return.
@@ -502,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         lA *= RowRef::step(lastA, refA.R);
                         lB *= RowRef::step(lastB, refB.R);
                     }
-                    const uint32_t lowA = refA.low(mA), lowB = refB.low(mB);
+                    const uint32_t lowA = refA.low(mA, 4.f), lowB = refB.low(mB, 4.f);
                     const float2 nA = make_float2(refA.minus(), refA.minus()), nB = make_float2(refB.minus(), refB.minus());
                     float2 sA = make_float2(0.f, 0.f), sB = sA;
                     uint32_t hiA[4], loA[4], hiB[4], loB[4];
@@ -519,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             a1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
                             sA = fma2(a0, i0, sA);
                             sA = fma2(a1, i1, sA);
-                            split4_p(a0.x, a0.y, a1.x, a1.y, lowA, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
+                            split4_p(a0.x, a0.y, a1.x, a1.y, lowA, lowA, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
                             float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
                             b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
                             b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
                             sB = fma2(b0, i0, sB);
                             sB = fma2(b1, i1, sB);
-                            split4_p(b0.x, b0.y, b1.x, b1.y, lowB, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
+                            split4_p(b0.x, b0.y, b1.x, b1.y, lowB, lowB, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
                         }
                     }
                     lA += sA.x + sA.y;

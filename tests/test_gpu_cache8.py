@@ -1,7 +1,7 @@
 """The 8-bit latent cache on the GPU: quantised append and read-back bit for bit, decode against 64 bits.
 
 Tolerances of decode8, from its roundings (u = 2^-8, half a bf16 step).  P is held by two terms within u of itself,
-or 2 u in the runs of 32 tokens where all are below the reference (their rounding is dithered);
+or 2 u in the runs of tokens where all are far below the reference (their rounding is dithered);
 probabilities far below the largest lose more of themselves, but alike in both directions over the tokens, so that
 their sum keeps within another u of the whole: 2 u in all.  With A = sum_t P_t |c_t| and d the error of
 a score (576 products summed in fp32: d <= 577 * 2^-23 * max_t sum |q_i c_ti| * scale), o_lat is off by at most
