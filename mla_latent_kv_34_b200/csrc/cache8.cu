@@ -145,8 +145,9 @@ __device__ __forceinline__ int read_tiles(const int32_t* kv_len, int b, int mb8,
 
 // The (sequence, quarter block) units are cut into equal ranges, one per CTA, so ragged lengths balance; a thread
 // takes four 16-byte units of codes (all four loads in flight) and writes two neighbouring 16-byte units of bf16 for
-// each.  Bound: HBM, 580 bytes read and 1152 written a token: 188 us for 520 K tokens, 3.2 TB/s of writes, where a plain fill
-// reaches 3.8 (32-byte stores changed nothing).
+// each.  Bound: HBM, 580 bytes read and 1152 written a token: 173 us for 520 K tokens, 5.1 TB/s (a copy 6.6, writes alone
+// 3.8).  Seven ranges an SM, of which four run at once: with 3, 4, 14 or 28 it took 178, 177, 177 and 183 us, with more
+// CTAs at once (fewer registers) 220 and more; with the addresses computed unit by unit 188.
 __global__ void __launch_bounds__(kReadThreads) read_cache8_kernel(
     const uint8_t* __restrict__ cache8, int64_t cap8, const int32_t* __restrict__ table8, int mb8,
     const int32_t* __restrict__ kv_len, int B, uint8_t* __restrict__ cache, int64_t cap, const int32_t* __restrict__ table,
@@ -189,6 +190,15 @@ __global__ void __launch_bounds__(kReadThreads) read_cache8_kernel(
         }
     }
     __syncthreads();
+    // this thread's units: one place of the rows rr, rr + 8, .. of a work unit (the swizzles repeat every eight rows), in
+    // latent chunk tid / 64 or, the last warp, in the RoPE part
+    const bool lat = tid < 256;
+    const int place = lat ? tid & 7 : tid & 3, rr = lat ? (tid >> 3) & 7 : lane >> 2;
+    const int v = lat ? 8 * (tid >> 6) + (place ^ rr) : 32 + (place ^ ((rr >> 1) & 3));  // columns 16 v .. 16 v + 15
+    const int src_row = lat ? 128 : 64;
+    const int src_off = (lat ? (tid >> 6) * kBlock8Chunk : kBlock8Rope) + rr * src_row + (place << 4);
+    const int dst_off = (v >> 2) * kBlockChunk + rr * 128;
+    const int at0 = (((2 * v) & 7) ^ rr) << 4, at1 = at0 ^ 16;
     const int64_t units = first[0] * kReadUnitsPerTile;
     const int64_t lo = units * blockIdx.x / gridDim.x, hi = units * (blockIdx.x + 1) / gridDim.x;
     int64_t tb = first[1] * kReadUnitsPerTile;
@@ -206,44 +216,31 @@ __global__ void __launch_bounds__(kReadThreads) read_cache8_kernel(
                 continue;
             }
             const uint8_t* src = cache8 + static_cast<int64_t>(e8) * kBlock8Bytes;
-            uint8_t* dst = cache + static_cast<int64_t>(e16) * kBlockBytes;
-            const int rows = min(kReadRows, L - t * kBlockTokens - row0);  // may be <= 0
-            // unit i of the 32 rows: 0..1023 latent (chunk i / 256, row i / 8 % 32, 16-byte place i % 8), then 128 of
-            // the RoPE part (row, place i % 4)
+            const float* sc = reinterpret_cast<const float*>(src + kBlock8Scales) + row0 + rr;
+            src += src_off + row0 * src_row;
+            uint8_t* dst = cache + static_cast<int64_t>(e16) * kBlockBytes + dst_off + row0 * 128;
+            const int rows = min(kReadRows, L - t * kBlockTokens - row0) - rr;  // row 8 k of this thread's: < rows
             uint4 x[4];
-            float s[4];
+            float f[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int i = tid + k * kReadThreads;
-                const bool lat = i < 1024;
-                const int rr = lat ? (i >> 3) & 31 : (i - 1024) >> 2;
                 x[k] = make_uint4(0, 0, 0, 0);
-                s[k] = 0.f;
-                if (rr < rows) {
-                    const int r = row0 + rr;
-                    const int off = lat ? (i >> 8) * kBlock8Chunk + r * 128 + ((i & 7) << 4)
-                                        : kBlock8Rope + r * 64 + ((i & 3) << 4);
-                    x[k] = *reinterpret_cast<const uint4*>(src + off);
-                    s[k] = *reinterpret_cast<const float*>(src + kBlock8Scales + 4 * r);
+                f[k] = 0.f;
+                if (8 * k < rows) {
+                    x[k] = *reinterpret_cast<const uint4*>(src + 8 * k * src_row);
+                    f[k] = sc[8 * k];
                 }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int i = tid + k * kReadThreads;
-                const bool lat = i < 1024;
-                const int rr = lat ? (i >> 3) & 31 : (i - 1024) >> 2;
-                if (rr >= rows) continue;
-                const int r = row0 + rr;
-                // columns 16 v .. 16 v + 15 of the row
-                const int v = lat ? 8 * (i >> 8) + ((i & 7) ^ (r & 7)) : 32 + ((i & 3) ^ ((r >> 1) & 3));
-                uint8_t* d = dst + (v >> 2) * kBlockChunk + r * 128;
-                const int u0 = (2 * v) & 7;
-                *reinterpret_cast<uint4*>(d + ((u0 ^ (r & 7)) << 4)) =
-                    make_uint4(two_back(x[k].x, s[k]), two_back(x[k].x >> 16, s[k]), two_back(x[k].y, s[k]),
-                               two_back(x[k].y >> 16, s[k]));
-                *reinterpret_cast<uint4*>(d + (((u0 + 1) ^ (r & 7)) << 4)) =
-                    make_uint4(two_back(x[k].z, s[k]), two_back(x[k].z >> 16, s[k]), two_back(x[k].w, s[k]),
-                               two_back(x[k].w >> 16, s[k]));
+                if (8 * k >= rows) continue;
+                uint8_t* d = dst + 8 * k * 128;
+                *reinterpret_cast<uint4*>(d + at0) =
+                    make_uint4(two_back(x[k].x, f[k]), two_back(x[k].x >> 16, f[k]), two_back(x[k].y, f[k]),
+                               two_back(x[k].y >> 16, f[k]));
+                *reinterpret_cast<uint4*>(d + at1) =
+                    make_uint4(two_back(x[k].z, f[k]), two_back(x[k].z >> 16, f[k]), two_back(x[k].w, f[k]),
+                               two_back(x[k].w >> 16, f[k]));
             }
         }
         tb = te;
@@ -268,7 +265,7 @@ cudaError_t launch_read_cache8(const uint8_t* cache8, int64_t cap8, const int32_
                                const int32_t* kv_len, int B, uint8_t* cache, int64_t cap, const int32_t* table, int mb16,
                                int32_t* dev_status, cudaStream_t stream) {
     const int64_t most = static_cast<int64_t>(B) * (mb8 < mb16 ? mb8 : mb16) * kReadUnitsPerTile;
-    const int64_t want = most < 148 * 7 ? most : 148 * 7;  // seven CTAs of nine warps fill an SM's 64 warps
+    const int64_t want = most < 148 * 7 ? most : 148 * 7;
     read_cache8_kernel<<<static_cast<unsigned>(want), kReadThreads, 0, stream>>>(cache8, cap8, table8, mb8, kv_len, B,
                                                                                  cache, cap, table, mb16, dev_status);
     return cudaGetLastError();
