@@ -307,7 +307,7 @@ def decode8(q, cache8, block_table, kv_len, W_UV, n_q: int, scale: float, num_sp
         _check(lib.mla_decode8(
             c.ptr(q, torch.bfloat16, (T, H, D_ROW), "q"), c.pool(cache8, BLOCK8_BYTES, "cache8"), cache8.shape[0],
             c.table(block_table, B), block_table.shape[1], c.ptr(kv_len, torch.int32, (B,), "kv_len"),
-            c.ptr(W_UV, torch.bfloat16, (H, D_H, D_C), "W_UV"), B, n_q, H, scale, num_splits,
+            c.ptr(W_UV, torch.bfloat16, (H, D_H, D_C), "W_UV"), B, n_q, H, float(scale), num_splits,
             c.ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size(),
             c.ptr(out, torch.bfloat16, (T, H, D_H), "out"), c.ptr(lse_out, torch.float32, (T, H), "lse_out"),
             c.ptr(dev_status, torch.int32, None, "dev_status"), c.raw))

@@ -261,7 +261,7 @@ def test_decode8_against_64_bits(lengths, H, n_q):
 @pytest.mark.parametrize("lengths,H,n_q", [
     ([1 + 7 * i % 300 for i in range(70)], 128, 1), ([3 + 11 * i % 170 for i in range(30)], 128, 3),
     ([40 + 29 * i % 200 for i in range(9)], 5, 40), ([130, 7], 100, 1), ([1500, 700, 40], 40, 1),
-    ([1400, 9, 513], 24, 1), ([700, 900], 16, 3)])
+    ([1400, 9, 513], 24, 1), ([700, 900], 16, 3), ([300, 257], 128, 256)])
 def test_decode8_many_rows_heads_and_pieces(lengths, H, n_q):
     """Blocks of query rows of several sequences, several blocks a head, rows that straddle the
     groups of 128, and one to three sequences a work unit."""
