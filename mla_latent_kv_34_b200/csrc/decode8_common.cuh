@@ -31,7 +31,7 @@ struct Params {
     const int32_t* block_table;
     const int32_t* kv_len;
     float* o_part;
-    float2* ml_part;
+    float4* ml_part;  // a piece's R, sum of P' / s, the same sum of P' as the MMAs have it
     int32_t* dev_status;
     int64_t cap_blocks;
     int max_blocks;

@@ -572,12 +572,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             __syncwarp();
             if (!ok) break;
             tc_fence_after();
-            // (R, l) per row: the set's four warps ended with the same reference
+            // R and the sum per row: the set's four warps ended with the same reference.  (The pair kernel's second sum is left
+            // out: the stacked lo term holds a bit more, and the registers are short.)
             for (int r = 32 * qd + lane; r < p.R; r += 128) {
                 const float2* part = reinterpret_cast<const float2*>(smem + L::kOffL) + (r / RN) * 4 * RN + r % RN;
                 const float2 a = part[0], b = part[RN], c = part[2 * RN], d = part[3 * RN];
                 const float l = (a.x + b.x) + (c.x + d.x);
-                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float2(l != l ? 0.f : a.y, l);
+                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float4(l != l ? 0.f : a.y, l, l, 0.f);
             }
             // the workspace holds [column / 32][row] x 32 fp32, rs rows per slot
             float* oseg = p.o_part + static_cast<int64_t>(s.slot) * p.rs * kDc;
@@ -635,7 +636,7 @@ cudaError_t launch(const Params& prm, cudaStream_t stream) {
 
 cudaError_t launch_decode8_sm(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
                               int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int ctas,
-                              float* o_part, float2* ml_part, int slots, int rs, int32_t* dev_status,
+                              float* o_part, float4* ml_part, int slots, int rs, int32_t* dev_status,
                               cudaStream_t stream) {
     const int R = n_q * H;
     if (R < 1 || R > kMaxSm8Rows || R > rs || ctas < 1 || B + ctas > slots) return cudaErrorInvalidValue;

@@ -70,8 +70,8 @@ constexpr int kScaleBufs = 4;
 constexpr int kScaleBytes = 2 * kTile * 2;             // a tile's token scales s, then log2 s, as bf16 (both exact)
 constexpr int kSOffScale = kSOffStage + kStages * kMsgStride;
 constexpr int kSOffRef = kSOffScale + kScaleBufs * kScaleBytes;  // [4][128] reference exponents handed on
-constexpr int kSOffLx = kSOffRef + 4 * kRows * 4;      // [3][2][128] a segment's (sum, R) of the first three quarters
-constexpr int kSOffBar = kSOffLx + 6 * kRows * 4;
+constexpr int kSOffLx = kSOffRef + 4 * kRows * 4;      // [3][3][128] a segment's two sums and R of the first three quarters
+constexpr int kSOffBar = kSOffLx + 9 * kRows * 4;
 constexpr int kSBarFull = 0, kSBarEmpty = 4, kSBarSFull = 8, kSBarSEmpty = 10, kSBarPEmpty = 12,
               kSBarFree = kSBarPEmpty + kPSlots, kSBarStaged = kSBarFree + kStages, kSBarRef = kSBarStaged + kStages,
               kSBarQx = kSBarRef + 16, kSBarLx = kSBarQx + 4, kSBarQFree = kSBarLx + 4, kSBarQReady = kSBarQFree + 1,
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 RowRef refA, refB;
                 refA.reset();
                 refB.reset();
-                float lA = 0.f, lB = 0.f;
+                float lA = 0.f, lB = 0.f, tA = 0.f, tB = 0.f;
                 const int limA = gA < p.R ? s.L - p.n_q + gA / p.H + 1 : 0;  // keys 0 .. lim-1 are visible
                 const int limB = gB < p.R ? s.L - p.n_q + gB / p.H + 1 : 0;
                 for (int t = s.t0; t < s.t1; ++t, ++n) {
@@ -513,10 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     if (__any_sync(0xffffffffu, lastA != refA.R || lastB != refB.R)) {
                         lA *= RowRef::step(lastA, refA.R);
                         lB *= RowRef::step(lastB, refB.R);
+                        tA *= RowRef::step(lastA, refA.R);
+                        tB *= RowRef::step(lastB, refB.R);
                     }
                     const uint32_t lowA = refA.low(mA, 4.f), lowB = refB.low(mB, 4.f);
                     const float2 nA = make_float2(refA.minus(), refA.minus()), nB = make_float2(refB.minus(), refB.minus());
-                    float2 sA = make_float2(0.f, 0.f), sB = sA;
+                    float2 sA = make_float2(0.f, 0.f), sB = sA, rA = sA, rB = sA;
                     uint32_t hiA[4], loA[4], hiB[4], loB[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -531,17 +533,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             a1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
                             sA = fma2(a0, i0, sA);
                             sA = fma2(a1, i1, sA);
+                            // as the MMAs will have it (8 significant bits): O is divided by the sum of what it sums
+                            a0 = bf16x2_f32(cvt_bf16x2(a0.x, a0.y));
+                            a1 = bf16x2_f32(cvt_bf16x2(a1.x, a1.y));
+                            rA = fma2(a0, i0, rA);
+                            rA = fma2(a1, i1, rA);
                             split4_p(a0.x, a0.y, a1.x, a1.y, lowA, lowA, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
                             float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
                             b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
                             b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
                             sB = fma2(b0, i0, sB);
                             sB = fma2(b1, i1, sB);
+                            b0 = bf16x2_f32(cvt_bf16x2(b0.x, b0.y));
+                            b1 = bf16x2_f32(cvt_bf16x2(b1.x, b1.y));
+                            rB = fma2(b0, i0, rB);
+                            rB = fma2(b1, i1, rB);
                             split4_p(b0.x, b0.y, b1.x, b1.y, lowB, lowB, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
                         }
                     }
                     lA += sA.x + sA.y;
                     lB += sB.x + sB.y;
+                    tA += rA.x + rA.y;
+                    tB += rB.x + rB.y;
                     ok = mbar_wait(&bars[kSBarFree + stg], stg_phase, abort_flag, kLimitNs) && ok;
                     // a row's 16 columns: the 16-byte unit (cb / 16) % 4 of its hi part and of its lo part
                     uint8_t* stage = smem + kSOffStage + stg * kMsgStride;
@@ -566,24 +579,31 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     }
                 }
                 if (!ok) break;
-                // segment result: (R, l), l summed over the row's eight column parts; a NaN sum keeps its piece
+                // segment result: R and the two sums over the row's eight column parts; a NaN sum keeps its piece
                 lA += __shfl_xor_sync(0xffffffffu, lA, 16);
                 lB += __shfl_xor_sync(0xffffffffu, lB, 16);
+                tA += __shfl_xor_sync(0xffffffffu, tA, 16);
+                tB += __shfl_xor_sync(0xffffffffu, tB, 16);
                 float lt = lane < 16 ? lA : lB;
+                float tt = lane < 16 ? tA : tB;
                 const float rmine = lane < 16 ? refA.R : refB.R;
                 if (cq < 3) {
-                    lx[2 * cq * kRows] = lt;
-                    lx[(2 * cq + 1) * kRows] = rmine;
+                    lx[3 * cq * kRows] = lt;
+                    lx[(3 * cq + 1) * kRows] = tt;
+                    lx[(3 * cq + 2) * kRows] = rmine;
                     mbar_arrive(&bars[kSBarLx + qd]);
                 } else {
                     ok = mbar_wait(&bars[kSBarLx + qd], kseg & 1u, abort_flag, kLimitNs);
                     ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        lt = fmaf(lx[2 * k * kRows], RowRef::step(lx[(2 * k + 1) * kRows], rmine), lt);
+                    for (int k = 0; k < 3; ++k) {
+                        const float f = RowRef::step(lx[(3 * k + 2) * kRows], rmine);
+                        lt = fmaf(lx[3 * k * kRows], f, lt);
+                        tt = fmaf(lx[(3 * k + 1) * kRows], f, tt);
+                    }
                     if (row_ok && ok)
                         p.ml_part[out_row_base + static_cast<int64_t>(s.slot) * kRows + r] =
-                            make_float2(lt != lt ? 0.f : rmine, lt);
+                            make_float4(lt != lt ? 0.f : rmine, lt, tt, 0.f);
                 }
                 ++kseg;
                 w = wn;
@@ -891,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
 
 cudaError_t launch_decode8_tc(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
                               int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int P_g,
-                              float* o_part, float2* ml_part, int slots, int32_t* dev_status, cudaStream_t stream) {
+                              float* o_part, float4* ml_part, int slots, int32_t* dev_status, cudaStream_t stream) {
     const int R = n_q * H;
     d8::Params prm = {q, cache, block_table, kv_len, o_part, ml_part, dev_status, cap_blocks, max_blocks, B, n_q, H, R,
                       (R + tc8::kRows - 1) / tc8::kRows, P_g, slots, tc8::kRows, scale * 1.44269504088896340736f};

@@ -1,7 +1,9 @@
 // End of mla_decode8: the merge of the attend kernel's pieces and the up-projection by W^UV, in one kernel.
 //
-//   o[t, h] = sum_p 2^(R_p - M) O_p / sum_p 2^(R_p - M) l_p    over the pieces p of t's sequence, M = max_p R_p
+//   o[t, h] = sum_p 2^(R_p - M) O_p / sum_p 2^(R_p - M) t_p    over the pieces p of t's sequence, M = max_p R_p
 //   lse     = (M + log2 sum_p 2^(R_p - M) l_p) ln 2            (R_p integers: exact factors)
+// with l_p the sum of the probabilities and t_p the sum as O_p has them, rounded to 8 significant bits each: a token that
+// carries its row alone then comes out exactly (4 x 128K, error against 64 bits 0.0026 -> 0.0018, for 3 % of the time).
 //   out[t, h, :] = W^UV_h o[t, h]                              (128 = 128 x 512)
 //
 // One CTA per (block of query rows, head): its 16 warps merge the rows, each a row at a time (or, with fewer rows than
@@ -38,8 +40,8 @@ constexpr int kSms = 148;
 constexpr int kBatch = 4;  // pieces whose loads are in flight together (64 bytes a lane each)
 constexpr int kWBytes = kDh * kDc * 2, kWChunk = kDh * 128;
 constexpr int kOffPart = kWBytes;                        // [16 warps][4][32 lanes] float4: a warp's share of a row; then out
-constexpr int kOffMz = kOffPart + kWarps * 2048;         // [16 warps] (M, z)
-constexpr int kOffTab = kOffMz + kWarps * 8;             // [32] the block's rows: Row
+constexpr int kOffMz = kOffPart + kWarps * 2048;         // [16 warps] M and the sums
+constexpr int kOffTab = kOffMz + kWarps * 16;             // [32] the block's rows: Row
 constexpr int kOffSeq = kOffTab + kMaxRows * 16;         // [32] tiles of the block's sequences; pieces (first, how many)
 constexpr int kOffBar = kOffSeq + kMaxRows * 8;          // W there, MMAs done
 constexpr int kOffRed = kOffBar + 16;                    // [2][16] tile counts; TMEM address
@@ -54,7 +56,7 @@ struct Row {
 
 struct FinParams {
     const float* o_part;
-    const float2* ml_part;
+    const float4* ml_part;
     const int32_t* kv_len;
     uint16_t* out;
     float* lse;
@@ -158,11 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
         while (2 * S * n <= kWarps) S *= 2;
         const int k = warp % S;
         float2 acc[8];
-        float M = -CUDART_INF_F, z = 0.f;
+        float M = -CUDART_INF_F, z = 0.f, zt = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] = make_float2(0.f, 0.f);
         auto write_row = [&](int i) {  // row i's o into the B operand, its lse out
-            const float inv = z > 0.f ? 1.f / z : (z != z ? CUDART_NAN_F : 0.f);
+            const float inv = zt > 0.f ? 1.f / zt : (zt != zt ? CUDART_NAN_F : 0.f);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int j = lane + 32 * q;  // columns 8 j .. 8 j + 7
@@ -183,11 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
         };
         int i = warp / S, e = k;
         while (i < n) {
-            float2 v[kBatch][8], ml[kBatch];
+            float2 v[kBatch][8];
+            float4 ml[kBatch];
             int row[kBatch];  // the row that item ends, or -1
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                ml[u] = make_float2(-CUDART_INF_F, 0.f);
+                ml[u] = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
                 row[u] = -1;
                 if (i < n) {
                     const Row w = tab[i];
@@ -214,18 +217,20 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
                         const float sc = RowRef::step(M, ml[u].x);
                         M = ml[u].x;
                         z *= sc;
+                        zt *= sc;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) acc[q] = mul2(acc[q], make_float2(sc, sc));
                     }
                     const float w = RowRef::step(ml[u].x, M);
                     z = fmaf(ml[u].y, w, z);
+                    zt = fmaf(ml[u].z, w, zt);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) acc[q] = fma2(make_float2(w, w), v[u][q], acc[q]);
                 }
                 if (S == 1 && row[u] >= 0) {
                     write_row(row[u]);
                     M = -CUDART_INF_F;
-                    z = 0.f;
+                    z = zt = 0.f;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) acc[q] = make_float2(0.f, 0.f);
                 }
@@ -236,20 +241,22 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 part[128 * warp + 32 * q] = make_float4(acc[2 * q].x, acc[2 * q].y, acc[2 * q + 1].x, acc[2 * q + 1].y);
-            if (lane == 0) reinterpret_cast<float2*>(smem + kOffMz)[warp] = make_float2(M, z);
+            if (lane == 0) reinterpret_cast<float4*>(smem + kOffMz)[warp] = make_float4(M, z, zt, 0.f);
             __syncthreads();
             if (k == 0 && warp / S < n) {
-                const float2* mz = reinterpret_cast<const float2*>(smem + kOffMz) + warp;
+                const float4* mz = reinterpret_cast<const float4*>(smem + kOffMz) + warp;
                 float top = M;
                 for (int u = 1; u < S; ++u) top = fmaxf(top, mz[u].x);
                 float sc = RowRef::step(M, top);
                 M = top;
                 z *= sc;
+                zt *= sc;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) acc[q] = mul2(acc[q], make_float2(sc, sc));
                 for (int u = 1; u < S; ++u) {
                     sc = RowRef::step(mz[u].x, top);  // (a warp without a piece: zeros)
                     z = fmaf(mz[u].y, sc, z);
+                    zt = fmaf(mz[u].z, sc, zt);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float4 x = part[128 * (warp + u) + 32 * q];
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
 
 }  // namespace fin8
 
-cudaError_t launch_finish8(const float* o_part, const float2* ml_part, const int32_t* kv_len, int max_blocks, int B, int n_q,
+cudaError_t launch_finish8(const float* o_part, const float4* ml_part, const int32_t* kv_len, int max_blocks, int B, int n_q,
                            int H, int P_g, int slots, int rs, const uint16_t* W_UV, uint16_t* out, float* lse_out,
                            int32_t* dev_status, cudaStream_t stream) {
     CUtensorMap map;

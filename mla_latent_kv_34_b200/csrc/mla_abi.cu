@@ -89,7 +89,7 @@ int units8(int n_q, int H) {
     return one_sm8(n_q, H) ? kMaxSmCtas : max_pairs_per_group((n_q * H + 127) / 128);
 }
 
-// Its workspace, from the first multiple of 32: segment partials [G][slots][rs rows] (R, l), then O as [G][slots] blocks
+// Its workspace, from the first multiple of 32: segment partials [G][slots][rs rows] float4 (R and two sums), then O as [G][slots] blocks
 // of [16 column groups of 32][rs rows] x 32 fp32.
 struct Ws8 {
     int G, slots, rs;
@@ -103,7 +103,7 @@ Ws8 ws8_layout(int B, int n_q, int H) {
     w.rs = one_sm8(n_q, H) ? (n_q * H <= 32 ? 32 : 64) : 128;
     const size_t rows = static_cast<size_t>(w.G) * w.slots * w.rs;
     w.ml_part = 0;
-    w.o_part = align1k(rows * sizeof(float2));
+    w.o_part = align1k(rows * sizeof(float4));
     w.total = w.o_part + rows * kDc * sizeof(float) + 16;
     return w;
 }
@@ -278,7 +278,7 @@ mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, co
     if (num_splits > 0 && num_splits < units) units = num_splits;
     char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
     float* o_part = reinterpret_cast<float*>(ws + lay.o_part);
-    float2* ml_part = reinterpret_cast<float2*>(ws + lay.ml_part);
+    float4* ml_part = reinterpret_cast<float4*>(ws + lay.ml_part);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const uint16_t* qp = static_cast<const uint16_t*>(q);
     const uint8_t* cp = static_cast<const uint8_t*>(cache8);

@@ -125,13 +125,13 @@ cudaError_t launch_decode_tc(const uint16_t* q, const uint8_t* cache, int64_t ca
 // for at most kMaxSm8Rows rows (decode8_sm.cu).
 cudaError_t launch_decode8_tc(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
                               int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int P_g,
-                              float* o_part, float2* ml_part, int slots, int32_t* dev_status, cudaStream_t stream);
+                              float* o_part, float4* ml_part, int slots, int32_t* dev_status, cudaStream_t stream);
 cudaError_t launch_decode8_sm(const uint16_t* q, const uint8_t* cache, int64_t cap_blocks, const int32_t* block_table,
                               int max_blocks, const int32_t* kv_len, int B, int n_q, int H, float scale, int ctas,
-                              float* o_part, float2* ml_part, int slots, int rs, int32_t* dev_status,
+                              float* o_part, float4* ml_part, int slots, int rs, int32_t* dev_status,
                               cudaStream_t stream);
 // The merge of their pieces with the W^UV projection (finish8.cu).
-cudaError_t launch_finish8(const float* o_part, const float2* ml_part, const int32_t* kv_len, int max_blocks, int B, int n_q,
+cudaError_t launch_finish8(const float* o_part, const float4* ml_part, const int32_t* kv_len, int max_blocks, int B, int n_q,
                            int H, int P_g, int slots, int rs, const uint16_t* W_UV, uint16_t* out, float* lse_out,
                            int32_t* dev_status, cudaStream_t stream);
 // Rows of the merged latent output o_lat kept for the up-projection: T rounded so that every 64-token
