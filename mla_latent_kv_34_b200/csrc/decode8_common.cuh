@@ -152,6 +152,11 @@ __device__ __forceinline__ void split4_q(uint32_t w0, uint32_t w1, float inv, ui
     lo = l0 | (static_cast<uint32_t>(l1) << 16);
 }
 
+// Two packed bf16 as fp32.
+__device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 // Packed fp32 arithmetic (two lanes an instruction).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
@@ -178,23 +183,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
-// What to add to each fp16 of a pair before its lower bits are cut off: `half` a step (rounding to nearest), or the dither
-// where `mask` is set.
-__device__ __forceinline__ uint32_t round_term(uint32_t mask, uint32_t dither, uint32_t half) {
-    return (mask & dither) | (~mask & half);
-}
-
-// Four probabilities 0 <= p <= 2^8.75 as hi (e4m3) and lo (e5m2) codes.  hi rounds to nearest; lo is what is left, in
-// e5m2's 3 significant bits: e5m2 is the upper half of an fp16, so an integer addition to the lower byte rounds it.  Down
-// to p = 2^-6 the pair holds p within 2^-8, like a bf16.  Below, hi's steps are 2^-9 and lo goes on to 2^-16, and many
-// equal small probabilities (a long tail behind one dominant token) would move their sum by up to an eighth if each were
-// rounded to nearest.  So where all of a row's probabilities in a unit of tokens are far below 1 (`mask`; the reference is
-// another unit's), lo's rounding is dithered over the tokens, which keeps the sum, at twice the error of each (2^-7).  Where
-// one is larger, its unit's tail cannot move the unit's sum by more than 2^-8: 31 times 2^-17 against 2^-4 in the pair
-// kernel's units, 127 times against 2^-2 in whole tiles.  (Dithered from 1 down, the error of a call was 0.0025 instead of
-// 0.0021; chosen by element, the attend phase took 92 us instead of 86.)
-__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t mask01, uint32_t mask23,
-                                         uint32_t dither01, uint32_t dither23, uint32_t& hi, uint32_t& lo) {
+// Four probabilities 0 <= p <= 2^8.75 of 8 significant bits (a bf16's) as hi (e4m3) and lo (e5m2) codes.  hi rounds to
+// nearest; what it leaves, at most 8 units of the last bit, has 3 significant bits, which e5m2 holds: exact down to
+// p = 2^-6.  Below, hi's steps are 2^-9 and lo goes on to 2^-16, and many equal small probabilities (a long tail behind one
+// dominant token) would move their sum by up to an eighth if each were rounded to nearest.  So lo's rounding is dithered
+// over the tokens, which keeps the sum: e5m2 is the upper half of an fp16, the dither is added to the lower byte before it
+// is cut off, and changes nothing where that byte is 0.
+__device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3, uint32_t dither01, uint32_t dither23,
+                                         uint32_t& hi, uint32_t& lo) {
     uint32_t h01, h23, d01, d23;
     uint16_t a, b;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(p1), "f"(p0));
@@ -204,9 +200,9 @@ __device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3,
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d01) : "r"(h01), "r"(e4m3x2_to_f16x2(a)));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d23) : "r"(h23), "r"(e4m3x2_to_f16x2(b)));
     hi = a | (static_cast<uint32_t>(b) << 16);
-    lo = __byte_perm(d01 + round_term(mask01, dither01, 0x00800080u), d23 + round_term(mask23, dither23, 0x00800080u), 0x7531);
+    lo = __byte_perm(d01 + dither01, d23 + dither23, 0x7531);
 }
-// The same with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant bits down
+// The same, for any p, with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant bits down
 // to 2^-10 and steps of 2^-13 below.  With the one bit more, a dithered rounding (`dither`: seven bits for each half) of
 // every probability still holds it within 2^-8.  An e4m3 code of x has the bits of the fp16 of 2^-8 x, less its top exponent bit and its last seven.
 __device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t dither, uint32_t& hi,
@@ -258,8 +254,6 @@ struct RowRef {
         return from == __uint_as_float(0xFF800000u) ? 1.f : factor(static_cast<int>(fmaxf(from - to, -127.f)));
     }
     __device__ __forceinline__ float minus() const { return R == __uint_as_float(0xFF800000u) ? 0.f : -R; }
-    // All ones where a unit's probabilities are all below 2^-k (round_term's mask).
-    __device__ __forceinline__ uint32_t low(float top, float k) const { return top < R - k ? 0xFFFFFFFFu : 0u; }
 };
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 operands (a_e5m2, b_e5m2: that one e5m2) and fp32 D.

@@ -57,7 +57,8 @@ struct Lay {
     static constexpr int kOffMax = kOffRowF + 4 * NR;        // [2 tiles][8 warps][kRN] row maxima
     static constexpr int kOffRef = kOffMax + 16 * kRN * 4;   // [8 warps][kRN] reference exponents, as the warp broadcasts them
     static constexpr int kOffL = kOffRef + 8 * kRN * 4;      // [8 warps][kRN] (sum, reference) of a segment
-    static constexpr int kOffBar = kOffL + 8 * kRN * 8;
+    static constexpr int kOffT = kOffL + 8 * kRN * 8;        // [8 warps][kRN] the second sum (not kStack)
+    static constexpr int kOffBar = kOffT + (kStack ? 0 : 8 * kRN * 4);
     static constexpr int kOffTail = kOffBar + kNumBars * 8;  // tmem base, abort flag, rescale place, [total, sequence, tile]
     static constexpr int kSmemBytes = kOffTail + 32;
     static_assert(2 * kN + 4 * kOC <= 512, "tensor memory");
@@ -378,11 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             tc_fence_before();
             mbar_arrive(&bars[kBQReady]);
             ok = mbar_wait(&bars[kBQReady], kseg & 1u, abort_flag, kLimitNs) && ok;  // every row's factor is there
-            float rowf[RN], lp[RN];
+            // sums of P' / s, and (where lo has 3 bits) of P' as the MMAs have it
+            float rowf[RN], lp[RN], tp[L::kStack ? 1 : RN];
 #pragma unroll
             for (int i = 0; i < RN; ++i) {
                 rowf[i] = rowf_all[row0 + i];
                 lp[i] = 0.f;
+                if (!L::kStack) tp[i] = 0.f;
             }
             uint32_t sc = scale_bits(e0, s.t0);
             RowRef ref;  // lane i < RN: row row0 + i
@@ -440,10 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 const int d = ref.move(top);
                 if (__any_sync(0xffffffffu, d != 0)) {
 #pragma unroll
-                    for (int i = 0; i < RN; ++i) lp[i] *= RowRef::factor(__shfl_sync(0xffffffffu, d, i));
+                    for (int i = 0; i < RN; ++i) {
+                        const float f = RowRef::factor(__shfl_sync(0xffffffffu, d, i));
+                        lp[i] *= f;
+                        if (!L::kStack) tp[i] *= f;
+                    }
                 }
                 if (lane < RN) refs[lane] = ref.R;
-                const uint32_t lows = L::kStack ? 0u : __ballot_sync(0xffffffffu, ref.low(top, 2.f) != 0);
                 __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
@@ -460,12 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     if (L::kStack) {
                         split4_p16(v[0], v[1], v[2], v[3], (dither >> 1) & 0x007F007Fu, hi[i / 4], lo[i / 4]);
                     } else {
-                        // (the four are one token's in four rows: the masks differ within a pair)
-                        uint32_t mask[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            mask[k] = ((lows >> (i + 2 * k)) & 1u ? 0x0000FFFFu : 0u) | ((lows >> (i + 2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
-                        split4_p(v[0], v[1], v[2], v[3], mask[0], mask[1], dither, dither, hi[i / 4], lo[i / 4]);
+                        const float2 a = bf16x2_f32(cvt_bf16x2(v[0], v[1])), b = bf16x2_f32(cvt_bf16x2(v[2], v[3]));
+                        tp[i] = fmaf(a.x, inv_s, tp[i]);
+                        tp[i + 1] = fmaf(a.y, inv_s, tp[i + 1]);
+                        tp[i + 2] = fmaf(b.x, inv_s, tp[i + 2]);
+                        tp[i + 3] = fmaf(b.y, inv_s, tp[i + 3]);
+                        split4_p(a.x, a.y, b.x, b.y, dither, dither, hi[i / 4], lo[i / 4]);
                     }
                 }
                 ok = mbar_wait(&bars[kBPFree + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs) && ok;
@@ -488,15 +494,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             // have been read
             if (kseg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars[kBOFree], (kseg - 1) & 1u, abort_flag, kLimitNs));
             if (!ok) break;
-            float sum = 0.f;
+            float sum = 0.f, tsum = 0.f;
 #pragma unroll
             for (int i = 0; i < RN; ++i) {
-                float v = lp[i];
+                float v = lp[i], t = L::kStack ? 0.f : tp[i];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == i) sum = v;
+                for (int o = 16; o > 0; o >>= 1) {
+                    v += __shfl_xor_sync(0xffffffffu, v, o);
+                    if (!L::kStack) t += __shfl_xor_sync(0xffffffffu, t, o);
+                }
+                if (lane == i) {
+                    sum = v;
+                    tsum = t;
+                }
             }
-            if (lane < RN) reinterpret_cast<float2*>(smem + L::kOffL)[warp * RN + lane] = make_float2(sum, ref.R);
+            if (lane < RN) {
+                reinterpret_cast<float2*>(smem + L::kOffL)[warp * RN + lane] = make_float2(sum, ref.R);
+                if (!L::kStack) reinterpret_cast<float*>(smem + L::kOffT)[warp * RN + lane] = tsum;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kBLReady]);
             ++kseg;
@@ -572,13 +587,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             __syncwarp();
             if (!ok) break;
             tc_fence_after();
-            // R and the sum per row: the set's four warps ended with the same reference.  (The pair kernel's second sum is left
-            // out: the stacked lo term holds a bit more, and the registers are short.)
+            // R and the sums per row: the set's four warps ended with the same reference
             for (int r = 32 * qd + lane; r < p.R; r += 128) {
-                const float2* part = reinterpret_cast<const float2*>(smem + L::kOffL) + (r / RN) * 4 * RN + r % RN;
+                const int at = (r / RN) * 4 * RN + r % RN;
+                const float2* part = reinterpret_cast<const float2*>(smem + L::kOffL) + at;
                 const float2 a = part[0], b = part[RN], c = part[2 * RN], d = part[3 * RN];
                 const float l = (a.x + b.x) + (c.x + d.x);
-                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float4(l != l ? 0.f : a.y, l, l, 0.f);
+                float t = l;  // (the stacked lo term holds a bit more: one sum serves for both)
+                if (!L::kStack) {
+                    const float* tp = reinterpret_cast<const float*>(smem + L::kOffT) + at;
+                    t = (tp[0] + tp[RN]) + (tp[2 * RN] + tp[3 * RN]);
+                }
+                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float4(l != l ? 0.f : a.y, l, t, 0.f);
             }
             // the workspace holds [column / 32][row] x 32 fp32, rs rows per slot
             float* oseg = p.o_part + static_cast<int64_t>(s.slot) * p.rs * kDc;

@@ -106,10 +106,6 @@ __device__ __forceinline__ float fmax16(const float (&v)[16]) {
     const float d = max3(v[9], v[10], v[11]), e = max3(v[12], v[13], v[14]);
     return fmaxf(max3(a, b, c), max3(d, e, v[15]));
 }
-// Two packed bf16 as fp32.
-__device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
 
 __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -516,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         tA *= RowRef::step(lastA, refA.R);
                         tB *= RowRef::step(lastB, refB.R);
                     }
-                    const uint32_t lowA = refA.low(mA, 4.f), lowB = refB.low(mB, 4.f);
                     const float2 nA = make_float2(refA.minus(), refA.minus()), nB = make_float2(refB.minus(), refB.minus());
                     float2 sA = make_float2(0.f, 0.f), sB = sA, rA = sA, rB = sA;
                     uint32_t hiA[4], loA[4], hiB[4], loB[4];
@@ -538,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             a1 = bf16x2_f32(cvt_bf16x2(a1.x, a1.y));
                             rA = fma2(a0, i0, rA);
                             rA = fma2(a1, i1, rA);
-                            split4_p(a0.x, a0.y, a1.x, a1.y, lowA, lowA, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
+                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
                             float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
                             b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
                             b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
@@ -548,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             b1 = bf16x2_f32(cvt_bf16x2(b1.x, b1.y));
                             rB = fma2(b0, i0, rB);
                             rB = fma2(b1, i1, rB);
-                            split4_p(b0.x, b0.y, b1.x, b1.y, lowB, lowB, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
+                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
                         }
                     }
                     lA += sA.x + sA.y;
