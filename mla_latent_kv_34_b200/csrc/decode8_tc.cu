@@ -9,7 +9,7 @@
 //     (decode8_common.cuh), so Q is exact and P keeps 8 significant bits; two K = 32 MMAs at twice the bf16 rate
 //     cost what the bf16 MMA of the same elements costs;
 //   - scores: y = S s_t (2^a scale log2 e) + log2 s_t with the query row's power of two 2^a; P' = 2^(y - R) carries
-//     s_t, because the rows of V are codes, and the row's sum takes P' / s_t.  R is RowRef's reference exponent;
+//     s_t, because the rows of V are codes, and the row's sums take P' / s_t.  R is RowRef's reference exponent;
 //   - a tile (72 KB of codes) comes as copies of 32 and 40 KB into a ring that holds two tiles, so a tile's copies are
 //     under way while the one before it is multiplied.
 // S CTA: the query's latent part in TMEM (hi 128 columns, lo 128 columns), its RoPE part in shared memory, two score

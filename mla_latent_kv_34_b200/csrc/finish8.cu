@@ -3,7 +3,7 @@
 //   o[t, h] = sum_p 2^(R_p - M) O_p / sum_p 2^(R_p - M) t_p    over the pieces p of t's sequence, M = max_p R_p
 //   lse     = (M + log2 sum_p 2^(R_p - M) l_p) ln 2            (R_p integers: exact factors)
 // with l_p the sum of the probabilities and t_p the sum as O_p has them, rounded to 8 significant bits each: a token that
-// carries its row alone then comes out exactly (4 x 128K, error against 64 bits 0.0026 -> 0.0018, for 3 % of the time).
+// carries its row alone then comes out exactly (4 x 128K, error against 64 bits 0.0026 -> 0.0018, for 2 to 3 % of the time).
 //   out[t, h, :] = W^UV_h o[t, h]                              (128 = 128 x 512)
 //
 // One CTA per (block of query rows, head): its 16 warps merge the rows, each a row at a time (or, with fewer rows than

@@ -1,9 +1,9 @@
 """The 8-bit latent cache on the GPU: quantised append and read-back bit for bit, decode against 64 bits.
 
-Tolerances of decode8, from its roundings (u = 2^-8, half a bf16 step).  P is held by two terms within u of itself,
-or 2 u in the runs of tokens where all are far below the reference (their rounding is dithered);
-probabilities far below the largest lose more of themselves, but alike in both directions over the tokens, so that
-their sum keeps within another u of the whole: 2 u in all.  With A = sum_t P_t |c_t| and d the error of
+Tolerances of decode8, from its roundings (u = 2^-8, half a bf16 step).  P is rounded to 8 significant bits (within u)
+or, in the one-SM kernel's 32-row form, to 9 with a dither (within u as well), and held by two terms; far below the
+reference their steps are absolute, and dithered over the tokens, so that the sum of a long tail keeps within another u
+of the whole: 2 u in all.  With A = sum_t P_t |c_t| and d the error of
 a score (576 products summed in fp32: d <= 577 * 2^-23 * max_t sum |q_i c_ti| * scale), o_lat is off by at most
 (2 u + 2 d + 2^-14) A (it is held by two bf16 terms, within 2^-16), and out is rounded to bf16:
     |out - ref| <= |W^UV| (2 u + 2 d + 2^-14) A + u |ref| (1 + 2^-7) + 2^-20,
