@@ -222,39 +222,71 @@ __device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p
     hi = a | (static_cast<uint32_t>(b) << 16);
     lo = __byte_perm(((d01 << 1) & 0x7F007F00u) | (d01 & 0x80008000u), ((d23 << 1) & 0x7F007F00u) | (d23 & 0x80008000u), 0x7531);
 }
-// The dither of token pair k of a thread's row part: two bytes of a low-discrepancy sequence (multiples of the golden
-// ratio), one in each half's lower byte.
-__host__ __device__ constexpr uint32_t dither_pair(int k) {
-    return ((static_cast<uint32_t>(2 * k) * 40503u + 20251u >> 8) & 0xFFu) |
-           (((static_cast<uint32_t>(2 * k + 1) * 40503u + 20251u >> 8) & 0xFFu) << 16);
+// The dither of token `tok` of tile t is an eight-bit number, base(tok) ^ mask(tok / 16, t): the 256 tokens of two tiles
+// have each of the 256 values once, so that even equal probabilities keep their sum down to 2^-24 (dithers of 16 levels, the
+// same in every tile, lost whole tails of equal probabilities below 2^-20).
+__host__ __device__ constexpr uint32_t rev4(uint32_t k) { return (k & 1) << 3 | (k & 2) << 1 | (k & 4) >> 1 | (k & 8) >> 3; }
+// base of tokens 2 k and 2 k + 1 of a run of 16, one in each half's lower byte.
+__host__ __device__ constexpr uint32_t dither_pair(int k) { return rev4(2 * k) << 4 | rev4(2 * k + 1) << 20; }
+// mask of run g (of 8) of tile t, in both halves.
+__device__ __forceinline__ uint32_t dither_mask(int g, int t) {
+    const uint32_t u = static_cast<uint32_t>(t);
+    return (rev4(static_cast<uint32_t>(g)) | (u & 1u) | ((u >> 1) * 176u & 0xF0u)) * 0x00010001u;
 }
 
 // The reference exponent of a row's probabilities, P' = 2^(y - R) with y = log2(p s_t) (s_t, the token's scale, is
-// folded into P because V's rows are codes).  O and the sum are kept relative to R, an integer, so moving it multiplies
-// them by an exact power of two.  P' has to stay below 448 (e4m3): R moves up when a unit's largest y - R exceeds 8.75, and
-// then (as at a piece's first tile) to where the largest P' lies in (1, 2].  It need not move down: a probability 2^-20 of
-// the largest is still held by the two terms, and 2^17 tokens below that are less than 1/8 of the sum.
-struct RowRef {
-    float R;
-    __device__ __forceinline__ void reset() { R = __uint_as_float(0xFF800000u); }
-    __device__ __forceinline__ bool must_move(float top) const { return top > R + 8.75f; }
-    // Takes a unit's largest y (-inf: nothing visible); returns the exponent by which O and the sum are to be multiplied
-    // (<= -126: they vanish), 0 for none.
-    __device__ __forceinline__ int move(float top) {
-        if (!must_move(top)) return 0;
-        const float to = ceilf(top) - 1.f;
-        // (no O yet: R is -inf, and nothing is multiplied)
-        const int d = (R == __uint_as_float(0xFF800000u)) ? 0 : static_cast<int>(fmaxf(R - to, -127.f));
-        R = to;
-        return d;
-    }
-    __device__ __forceinline__ static float factor(int d) { return d <= -126 ? 0.f : exp2_int(d); }
-    // The factor from one reference to another (1 where there was none: the sum is then 0).
-    __device__ __forceinline__ static float step(float from, float to) {
-        return from == __uint_as_float(0xFF800000u) ? 1.f : factor(static_cast<int>(fmaxf(from - to, -127.f)));
-    }
-    __device__ __forceinline__ float minus() const { return R == __uint_as_float(0xFF800000u) ? 0.f : -R; }
+// folded into P because V's rows are codes).  O and the sums are kept relative to R, an integer, so moving it multiplies
+// them by an exact power of two.  The terms' steps are absolute (2^-16 and 2^-13), P' has to stay below 448, and one token
+// may be far above tens of thousands that share the rest of the sum.  So the largest P' belongs near the top, where the
+// steps are 2^-21 of it and less; but a row whose first units are its first of many alike needs room to rise, since every
+// move costs the whole tile a pass over O.  A row's units (the tokens whose largest y is known at once) follow one another:
+//   first  its largest P' goes to (2^(First - 1), 2^First];
+//   up     when a unit's largest y passes R + 8.75: its largest P' goes to (2^(Up - 1), 2^Up];
+//   down   when the largest P' of two units running (two of the same warp's turns, R the same at both) lies below 2^-Low, what
+//          set R was a peak: R moves down, First powers of two below the larger one, but only until the peak is at 2^Up.
+// With R fixed at the first unit's largest P' in (1, 2], 32 K tokens 2^9 below the first cost 0.007 of the result in the 2-norm
+// (0.013 with the 2^-13 steps), and 0.03 (0.07) where the first token's scale was 8 times theirs; now 0.004 at most.
+constexpr uint32_t kMinusInf = 0xFF800000u;
+constexpr uint32_t kNoTile = 0xFFFFFFFEu;
+struct LowUnit {  // a warp's last low unit of a row: its largest y, its tile (counted over the work unit; kNoTile: none)
+    float top;
+    uint32_t at;
 };
+template <int First, int Up, int Low>
+struct RowRef {
+    __device__ static bool is_up(float top, float R) { return top > R + 8.75f; }
+    // (not for a unit with nothing visible, nor before the first)
+    __device__ static bool is_low(float top, float R) {
+        return top < R - static_cast<float>(Low) && top != __uint_as_float(kMinusInf);
+    }
+    // The reference after a unit of tile n whose largest y is `top`; `same`: R has not changed since this warp's last unit,
+    // of tile n - 1.  `low` is the warp's for the row, `peak` the y (rounded up) that the row's last first or up move was for.
+    __device__ static float moved(float top, float R, bool same, uint32_t n, LowUnit& low, float& peak) {
+        if (is_up(top, R)) {
+            peak = ceilf(top);
+            return peak - (R == __uint_as_float(kMinusInf) ? First : Up);
+        }
+        if (!is_low(top, R)) return R;
+        if (same && low.at == n - 1) {
+            low.at = kNoTile;
+            return fminf(R, fmaxf(ceilf(fmaxf(top, low.top)) - First, peak - Up));
+        }
+        low.top = top;
+        low.at = n;
+        return R;
+    }
+};
+// The exponent by which O and the sums are multiplied when R moves (<= -126: they vanish; 0 too where there was none).
+__device__ __forceinline__ int ref_exp(float from, float to) {
+    return from == __uint_as_float(kMinusInf) ? 0 : static_cast<int>(fmaxf(from - to, -127.f));
+}
+__device__ __forceinline__ float ref_factor(int d) { return d <= -126 ? 0.f : exp2_int(d); }
+// The factor from one reference to another (1 where there was none: the sum is then 0).
+__device__ __forceinline__ float ref_step(float from, float to) {
+    return from == __uint_as_float(kMinusInf) ? 1.f : ref_factor(static_cast<int>(fmaxf(from - to, -127.f)));
+}
+// What is added to y (0 where there is no reference yet: y is -inf then).
+__device__ __forceinline__ float ref_minus(float R) { return R == __uint_as_float(kMinusInf) ? 0.f : -R; }
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 operands (a_e5m2, b_e5m2: that one e5m2) and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false,

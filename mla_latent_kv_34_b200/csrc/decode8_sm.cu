@@ -74,6 +74,10 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, int32_t* d
     if (dev_status) atomicOr(dev_status, MLA_DEVERR_TIMEOUT);
 }
 
+// A unit is a tile of a row.  The largest P' of the first 128 tokens goes into (8, 16]: few rows rise 2^5 above that, a move is
+// cheaper here (at most 48 rows), and the stacked lo term's steps (2^-13) are then 2^-16 of the largest.
+using Ref = RowRef<4, 6, 3>;
+
 // Maximum over the warp's 32 lanes (NaN only if all are).
 __device__ __forceinline__ float warp_max_f32(float v) {
     float r;
@@ -305,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * qd) << 16);
         float* refs = reinterpret_cast<float*>(smem + L::kOffRef) + warp * RN;
         const float* rowf_all = reinterpret_cast<const float*>(smem + L::kOffRowF);
-        // the token's dither (multiples of the golden ratio over the tokens), for both halves of a pair of rows
-        const uint32_t dither = (((static_cast<uint32_t>(tk) * 40503u + 20251u) >> 8) & 0xFFu) * 0x00010001u;
+        // the token's dither, for both halves of a pair of rows, but for what depends on the tile
+        const uint32_t dither0 = (rev4(tk & 15) << 4) * 0x00010001u;
         SegWalk w = walk;
         Seg s;
         uint32_t n = 0, kseg = 0;
@@ -388,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 if (!L::kStack) tp[i] = 0.f;
             }
             uint32_t sc = scale_bits(e0, s.t0);
-            RowRef ref;  // lane i < RN: row row0 + i
-            ref.reset();
+            float R = -CUDART_INF_F, peak = R;  // lane i < RN: row row0 + i's reference and peak
+            LowUnit low = {0.f, kNoTile};
             const int lim0 = s.L - p.n_q + 1;  // keys below this are visible to every query of the step
             for (int t = s.t0; t < s.t1; ++t, ++n) {
                 const uint32_t sb = n & 1u, us = n >> 1;
@@ -440,16 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 if (lane < RN && row0 + lane < p.R)
                     top = fmaxf(fmaxf(mx[lane], mx[RN + lane]), fmaxf(mx[2 * RN + lane], mx[3 * RN + lane]));
                 else top = -CUDART_INF_F;
-                const int d = ref.move(top);
+                const uint32_t dither = dither0 ^ dither_mask(tk >> 4, t);
+                int d = 0;
+                if (__any_sync(0xffffffffu, Ref::is_up(top, R) || Ref::is_low(top, R))) {
+                    const float was = R;
+                    R = Ref::moved(top, R, t > s.t0, n, low, peak);
+                    d = ref_exp(was, R);
+                }
                 if (__any_sync(0xffffffffu, d != 0)) {
 #pragma unroll
                     for (int i = 0; i < RN; ++i) {
-                        const float f = RowRef::factor(__shfl_sync(0xffffffffu, d, i));
+                        const float f = ref_factor(__shfl_sync(0xffffffffu, d, i));
                         lp[i] *= f;
                         if (!L::kStack) tp[i] *= f;
                     }
                 }
-                if (lane < RN) refs[lane] = ref.R;
+                if (lane < RN) refs[lane] = R;
                 __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 }
             }
             if (lane < RN) {
-                reinterpret_cast<float2*>(smem + L::kOffL)[warp * RN + lane] = make_float2(sum, ref.R);
+                reinterpret_cast<float2*>(smem + L::kOffL)[warp * RN + lane] = make_float2(sum, R);
                 if (!L::kStack) reinterpret_cast<float*>(smem + L::kOffT)[warp * RN + lane] = tsum;
             }
             __syncwarp();
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     for (int r = 0; r < NR; r += 8) {
                         float f[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = RowRef::factor(dd[r + k]);
+                        for (int k = 0; k < 8; ++k) f[k] = ref_factor(dd[r + k]);
 #pragma unroll
                         for (int part = 0; part < L::kOC / NR; ++part) {  // hi columns, lo columns
                             uint32_t v[4][8];

@@ -71,7 +71,9 @@ constexpr int kScaleBytes = 2 * kTile * 2;             // a tile's token scales 
 constexpr int kSOffScale = kSOffStage + kStages * kMsgStride;
 constexpr int kSOffRef = kSOffScale + kScaleBufs * kScaleBytes;  // [4][128] reference exponents handed on
 constexpr int kSOffLx = kSOffRef + 4 * kRows * 4;      // [3][3][128] a segment's two sums and R of the first three quarters
-constexpr int kSOffBar = kSOffLx + 9 * kRows * 4;
+constexpr int kSOffPeak = kSOffLx + 9 * kRows * 4;     // [128] a row's peak (RowRef)
+constexpr int kSOffLow = kSOffPeak + kRows * 4;        // [16 warps][32] LowUnit
+constexpr int kSOffBar = kSOffLow + kSoftWarps * 32 * 8;
 constexpr int kSBarFull = 0, kSBarEmpty = 4, kSBarSFull = 8, kSBarSEmpty = 10, kSBarPEmpty = 12,
               kSBarFree = kSBarPEmpty + kPSlots, kSBarStaged = kSBarFree + kStages, kSBarRef = kSBarStaged + kStages,
               kSBarQx = kSBarRef + 16, kSBarLx = kSBarQx + 4, kSBarQFree = kSBarLx + 4, kSBarQReady = kSBarQFree + 1,
@@ -99,6 +101,10 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t p
     st_cluster_u32(peer_abort, 1u);
     if (dev_status) atomicOr(dev_status, MLA_DEVERR_TIMEOUT);
 }
+
+// A unit is 32 tokens of a row.  The first one's largest P' goes into (1, 2]: a flat row then has 7 powers of two to rise
+// before R moves (B 32, H 128, 8K: 124 us with 5 and 161 with 3, instead of 108).
+using Ref = RowRef<1, 6, 6>;
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float fmax16(const float (&v)[16]) {
@@ -314,6 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             SegWalk w = walk, wn;
             Seg s, sn;
             uint32_t n = 0, kseg = 0, nref = 0;  // tiles, segments, references received
+            // a row's state where its reference moves; both in shared memory, since moves are rare and registers are not
+            LowUnit& low = reinterpret_cast<LowUnit*>(smem + kSOffLow)[32 * warp + lane];
+            float& peak = reinterpret_cast<float*>(smem + kSOffPeak)[r];
+            low.at = kNoTile;
             uint32_t stg = cq >> 1, stg_phase = 1;  // the staging buffer of message 2 n + cq / 2, and the phase it is free in
             bool ok = true;
             bool have = w.next(p, s);
@@ -432,9 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 // tokens' scales are then read and unpacked once for two rows
                 const float rowfA = __shfl_sync(0xffffffffu, rowf, lane & 15), rowfB = __shfl_sync(0xffffffffu, rowf, 16 + (lane & 15));
                 const float2 fA = make_float2(rowfA, rowfA), fB = make_float2(rowfB, rowfB);
-                RowRef refA, refB;
-                refA.reset();
-                refB.reset();
+                float RA = -CUDART_INF_F, RB = RA, R = RA;  // the references of rows rA, rB and 32 qd + lane
                 float lA = 0.f, lB = 0.f, tA = 0.f, tB = 0.f;
                 const int limA = gA < p.R ? s.L - p.n_q + gA / p.H + 1 : 0;  // keys 0 .. lim-1 are visible
                 const int limB = gB < p.R ? s.L - p.n_q + gB / p.H + 1 : 0;
@@ -489,30 +497,37 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 16));
                     mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 16));
                     // the reference: the previous unit's (another warp's), moved if this unit needs it, handed on
-                    const float lastA = refA.R, lastB = refB.R;
+                    const float lastA = RA, lastB = RB;
                     if (cq > 0 || t > s.t0) {
                         ok = mbar_wait(bar_in, nref & 1u, abort_flag, kLimitNs) && ok;
                         ++nref;
-                        refA.R = ref_in[lane & 15];
-                        refB.R = ref_in[16 + (lane & 15)];
+                        RA = ref_in[lane & 15];
+                        RB = ref_in[16 + (lane & 15)];
                     }
-                    int dA = 0, dB = 0;
-                    if (__any_sync(0xffffffffu, refA.must_move(mA) || refB.must_move(mB))) {
-                        dA = refA.move(mA);
-                        dB = refB.move(mB);
+                    const float top = lane < 16 ? mA : mB;
+                    R = lane < 16 ? RA : RB;
+                    int d = 0;
+                    if (__any_sync(0xffffffffu, Ref::is_up(top, R) || Ref::is_low(top, R))) {
+                        const float was = R;
+                        R = Ref::moved(top, R, R == (lane < 16 ? lastA : lastB), n, low, peak);
+                        d = ref_exp(was, R);
+                        RA = __shfl_sync(0xffffffffu, R, lane & 15);
+                        RB = __shfl_sync(0xffffffffu, R, 16 + (lane & 15));
                     }
                     if (cq < 3 || t + 1 < s.t1) {
-                        ref_out[lane] = lane < 16 ? refA.R : refB.R;
+                        ref_out[lane] = R;
                         mbar_arrive(bar_out);
                     }
                     // the sums are relative to the reference of this warp's last unit
-                    if (__any_sync(0xffffffffu, lastA != refA.R || lastB != refB.R)) {
-                        lA *= RowRef::step(lastA, refA.R);
-                        lB *= RowRef::step(lastB, refB.R);
-                        tA *= RowRef::step(lastA, refA.R);
-                        tB *= RowRef::step(lastB, refB.R);
+                    if (__any_sync(0xffffffffu, lastA != RA || lastB != RB)) {
+                        const float a = ref_step(lastA, RA), b = ref_step(lastB, RB);
+                        lA *= a;
+                        tA *= a;
+                        lB *= b;
+                        tB *= b;
                     }
-                    const float2 nA = make_float2(refA.minus(), refA.minus()), nB = make_float2(refB.minus(), refB.minus());
+                    const float2 nA = make_float2(ref_minus(RA), ref_minus(RA)), nB = make_float2(ref_minus(RB), ref_minus(RB));
+                    const uint32_t dm = dither_mask(cb >> 4, t);
                     float2 sA = make_float2(0.f, 0.f), sB = sA, rA = sA, rB = sA;
                     uint32_t hiA[4], loA[4], hiB[4], loB[4];
 #pragma unroll
@@ -533,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             a1 = bf16x2_f32(cvt_bf16x2(a1.x, a1.y));
                             rA = fma2(a0, i0, rA);
                             rA = fma2(a1, i1, rA);
-                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiA[o], loA[o]);
+                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2) ^ dm, dither_pair(c / 2 + 1) ^ dm, hiA[o], loA[o]);
                             float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
                             b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
                             b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
@@ -543,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             b1 = bf16x2_f32(cvt_bf16x2(b1.x, b1.y));
                             rB = fma2(b0, i0, rB);
                             rB = fma2(b1, i1, rB);
-                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2), dither_pair(c / 2 + 1), hiB[o], loB[o]);
+                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2) ^ dm, dither_pair(c / 2 + 1) ^ dm, hiB[o], loB[o]);
                         }
                     }
                     lA += sA.x + sA.y;
@@ -560,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     *reinterpret_cast<uint4*>(ah + 2048) = make_uint4(hiB[0], hiB[1], hiB[2], hiB[3]);
                     *reinterpret_cast<uint4*>(al) = make_uint4(loA[0], loA[1], loA[2], loA[3]);
                     *reinterpret_cast<uint4*>(al + 2048) = make_uint4(loB[0], loB[1], loB[2], loB[3]);
-                    reinterpret_cast<int8_t*>(stage + kPBytes)[(cq & 1) * kRows + r] = static_cast<int8_t>(lane < 16 ? dA : dB);
+                    reinterpret_cast<int8_t*>(stage + kPBytes)[(cq & 1) * kRows + r] = static_cast<int8_t>(d);
                     fence_proxy_async_cta();
                     mbar_arrive(&bars[kSBarStaged + stg]);
                     stg += 2;
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 tB += __shfl_xor_sync(0xffffffffu, tB, 16);
                 float lt = lane < 16 ? lA : lB;
                 float tt = lane < 16 ? tA : tB;
-                const float rmine = lane < 16 ? refA.R : refB.R;
+                const float rmine = R;
                 if (cq < 3) {
                     lx[3 * cq * kRows] = lt;
                     lx[(3 * cq + 1) * kRows] = tt;
@@ -592,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
-                        const float f = RowRef::step(lx[(3 * k + 2) * kRows], rmine);
+                        const float f = ref_step(lx[(3 * k + 2) * kRows], rmine);
                         lt = fmaf(lx[3 * k * kRows], f, lt);
                         tt = fmaf(lx[(3 * k + 1) * kRows], f, tt);
                     }
@@ -832,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         const int d =
                             reinterpret_cast<const int8_t*>(smem + kOOffMsg + kPBytes + *resc_pb)[r];
                         if (__any_sync(0xffffffffu, d != 0)) {
-                            const float a = RowRef::factor(d);
+                            const float a = ref_factor(d);
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
                                 uint32_t v[32];

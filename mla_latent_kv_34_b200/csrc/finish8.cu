@@ -214,14 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
             for (int u = 0; u < kBatch; ++u) {
                 if (ml[u].x != -CUDART_INF_F) {
                     if (ml[u].x > M) {
-                        const float sc = RowRef::step(M, ml[u].x);
+                        const float sc = ref_step(M, ml[u].x);
                         M = ml[u].x;
                         z *= sc;
                         zt *= sc;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) acc[q] = mul2(acc[q], make_float2(sc, sc));
                     }
-                    const float w = RowRef::step(ml[u].x, M);
+                    const float w = ref_step(ml[u].x, M);
                     z = fmaf(ml[u].y, w, z);
                     zt = fmaf(ml[u].z, w, zt);
 #pragma unroll
@@ -247,14 +247,14 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
                 const float4* mz = reinterpret_cast<const float4*>(smem + kOffMz) + warp;
                 float top = M;
                 for (int u = 1; u < S; ++u) top = fmaxf(top, mz[u].x);
-                float sc = RowRef::step(M, top);
+                float sc = ref_step(M, top);
                 M = top;
                 z *= sc;
                 zt *= sc;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) acc[q] = mul2(acc[q], make_float2(sc, sc));
                 for (int u = 1; u < S; ++u) {
-                    sc = RowRef::step(mz[u].x, top);  // (a warp without a piece: zeros)
+                    sc = ref_step(mz[u].x, top);  // (a warp without a piece: zeros)
                     z = fmaf(mz[u].y, sc, z);
                     zt = fmaf(mz[u].z, sc, zt);
 #pragma unroll

@@ -115,3 +115,21 @@ def test_binding_refuses_wrong_tensors(mla):
     with pytest.raises(mla.MLAError):
         mla.append_cache8(pool, tab, one, one, torch.zeros(1, 512, dtype=torch.bfloat16),
                           torch.zeros(1, 64, dtype=torch.bfloat16), torch.zeros(4, 64))
+
+
+@pytest.mark.parametrize("mass", [0.05, 0.2, 0.5])
+def test_peaked_cases_show_a_lost_tail(mass):
+    """The cases of test_gpu_cache8_peaked.py fail where the tail's probabilities are dropped from o but not from its sum."""
+    from cache8_cases import L2, peaked_queries, peaked_rows
+    x = peaked_rows(8000, mass)
+    codes, s = o8.quantise(x)
+    rows, q = o8.VALUES[codes] * s[:, None], peaked_queries((1, 2))
+    W = np.random.default_rng(1).standard_normal((2, 128, 512)) / np.sqrt(512)
+    out, _, o, A, _ = o8.attend(rows, q, W, 1, 192 ** -0.5)
+    a = q[0] @ rows.T / np.sqrt(192.0)
+    p = np.exp(a - a.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    # (the peak's score, below 16, is rounded by 2^-4 of itself at most, the scores' other columns add less than 0.1)
+    assert np.abs(np.log(p[:, 1:].sum(1) / mass)).max() < 1.1
+    lost = np.einsum("hc,hdc->hd", p[:, :1] * rows[0, :512], W)
+    assert np.linalg.norm(lost - out[0]) > 1.5 * L2 * np.linalg.norm(out)
