@@ -222,16 +222,15 @@ __device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p
     hi = a | (static_cast<uint32_t>(b) << 16);
     lo = __byte_perm(((d01 << 1) & 0x7F007F00u) | (d01 & 0x80008000u), ((d23 << 1) & 0x7F007F00u) | (d23 & 0x80008000u), 0x7531);
 }
-// The dither of token `tok` of tile t is an eight-bit number, base(tok) ^ mask(tok / 16, t): the 256 tokens of two tiles
-// have each of the 256 values once, so that even equal probabilities keep their sum down to 2^-24 (dithers of 16 levels, the
-// same in every tile, lost whole tails of equal probabilities below 2^-20).
+// The dither of token `tok` of tile t is an eight-bit number, base(tok % 16) + mask(tok / 16, t), the base a multiple of 16 and
+// the mask below it: the 256 tokens of two tiles have each of the 256 values once, so that even equal probabilities keep
+// their sum down to 2^-24 (dithers of 16 levels, the same in every tile, lost whole tails of equal probabilities below 2^-20).
 __host__ __device__ constexpr uint32_t rev4(uint32_t k) { return (k & 1) << 3 | (k & 2) << 1 | (k & 4) >> 1 | (k & 8) >> 3; }
 // base of tokens 2 k and 2 k + 1 of a run of 16, one in each half's lower byte.
 __host__ __device__ constexpr uint32_t dither_pair(int k) { return rev4(2 * k) << 4 | rev4(2 * k + 1) << 20; }
 // mask of run g (of 8) of tile t, in both halves.
 __device__ __forceinline__ uint32_t dither_mask(int g, int t) {
-    const uint32_t u = static_cast<uint32_t>(t);
-    return (rev4(static_cast<uint32_t>(g)) | (u & 1u) | ((u >> 1) * 176u & 0xF0u)) * 0x00010001u;
+    return rev4(static_cast<uint32_t>(g)) * 0x00010001u + (static_cast<uint32_t>(t) & 1u) * 0x00010001u;
 }
 
 // The reference exponent of a row's probabilities, P' = 2^(y - R) with y = log2(p s_t) (s_t, the token's scale, is
@@ -241,57 +240,178 @@ __device__ __forceinline__ uint32_t dither_mask(int g, int t) {
 // steps are 2^-21 of it and less; but a row whose first units are its first of many alike needs room to rise, since every
 // move costs the whole tile a pass over O.  A row's units (the tokens whose largest y is known at once) follow one another:
 //   first  its largest P' goes to (2^(First - 1), 2^First];
-//   up     when a unit's largest y passes R + 8.75: its largest P' goes to (2^(Up - 1), 2^Up];
+//   up     when a unit's largest y passes R + 8.75 (kRoom): its largest P' goes to (2^(Up - 1), 2^Up];
 //   down   when the largest P' of two units running (two of the same warp's turns, R the same at both) lies below 2^-Low, what
-//          set R was a peak: R moves down, First powers of two below the larger one, but only until the peak is at 2^Up.
+//          set R was a peak: R moves down, First powers of two below the larger one, but only until the peak is at 2^Up;
+//   eager  (TileAsks) the first such unit moves R, at most 2^kLift below the highest R of the piece: O and the sums,
+//          P' / s with s >= 2^-40 among them, then stay finite in fp32, and what is lost is below 2^-kLift of the largest.
 // With R fixed at the first unit's largest P' in (1, 2], 32 K tokens 2^9 below the first cost 0.007 of the result in the 2-norm
 // (0.013 with the 2^-13 steps), and 0.03 (0.07) where the first token's scale was 8 times theirs; now 0.004 at most.
 constexpr uint32_t kMinusInf = 0xFF800000u;
+constexpr float kNoRef = -3.402823466e38f;  // no reference yet: the lowest float; y - kNoRef is -inf where y is
 constexpr uint32_t kNoTile = 0xFFFFFFFEu;
 struct LowUnit {  // a warp's last low unit of a row: its largest y, its tile (counted over the work unit; kNoTile: none)
     float top;
     uint32_t at;
 };
+// What a tile's rows ask of R.  A row's scale covers its RoPE columns, and is 1 for a row of zeros, so a token may have a large
+// y and add little or nothing to O, while the others in its unit are held in steps set by it.  So one warp looks at the
+// rows ahead of the softmax: at 16 of each token's latent codes, and at all of them where those are below 448 * 2^-7.8.
+//   f     the exponent of a token's largest latent code against 448, less the largest such in the tile, added to its y where
+//         R is chosen.  -7 at least: with R + 1.75 instead of R + 8.75 as the limit of y + f (`room`), its P' stays below 448.
+//         Used where some f is -4 or less, or some token's latents are all zero: such a token has no P' to hold, so its y is
+//         taken kZeroDown lower everywhere (so that its P' is small and sets nothing) but in the sums; its f is kZeroF.
+//   eager what set R may have been large by its scale alone: f are in use, or were in the tile before, or its latents were all
+//         small against their scales, or the scales have fallen by 2^4 since this last was so.  Low units move R at once.
+// 511 rows of standard deviation a and one of zeros in their midst lost 0.06 of the result at a = 0.01, all of it at 1e-5.
+constexpr float kRoom = 8.75f, kRoomF = 1.75f;
+constexpr int kFar = 4;
+constexpr float kZeroF = 1.f, kZeroDown = 40.f;
+struct TileAsks {
+    float half;  // RowRef::stays: negative where f are in use
+    uint32_t with_f, eager, pad;
+    __device__ __forceinline__ float room() const { return with_f ? kRoomF : kRoom; }
+};
+// f of a token whose largest latent code (sign dropped) is `top`.
+__device__ __forceinline__ int code_exp(uint32_t top) {  // (0x7E is 448)
+    return min(static_cast<int>(top >> 3) - 15 + ((top & 7u) == 7u ? 1 : 0), 0);
+}
+constexpr int kNoLatent = -99;
+constexpr uint32_t kNoScale = 0x0D800000u;  // 2^-100, for tokens that do not exist (their scores are masked)
+// The largest of 16 codes, signs dropped.
+__device__ __forceinline__ uint32_t max_code16(uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m = __vmaxu2(m, w[i] & 0x7F007F00u);
+        m = __vmaxu2(m, (w[i] << 8) & 0x7F007F00u);
+    }
+    return max((m >> 8) & 0x7Fu, m >> 24);
+}
+// One warp judges the tiles of a segment one after another, from the codes that the copies brought to shared memory.  (The
+// code of the common case is kept short: the loops of a block's warps share an instruction cache that they fill.)
+struct TileJudge {
+    int run;      // largest scale since the last eager tile
+    bool before;  // the tile before may have set R by its scales
+    __device__ __forceinline__ void reset() {
+        run = -1000;
+        before = false;
+    }
+    // The tile's codes are at `tile`, its first n >= 1 tokens exist; `bits`: the scales of tokens 4 lane .. 4 lane + 3 (kNoScale for
+    // those that do not).  f of those, as described, four int8, where they are in use.
+    __device__ __forceinline__ TileAsks judge(const uint8_t* tile, int n, const uint32_t (&bits)[4], int lane, float half, uint32_t& f) {
+        // 16 codes of a token, none of which is 2 = 448 * 2^-7.8 or more: the upper exponent bit is not set
+        const uint8_t* at = tile + lane * 128;
+        bool small = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // units that spread over the banks, and over the columns
+            const uint4 x = *reinterpret_cast<const uint4*>(at + i * 4096 + (((lane + (lane >> 3) + 4 * i) & 7) << 4));
+            small = small || (((x.x | x.y | x.z | x.w) & 0x40404040u) == 0 && 32 * i + lane < n);
+        }
+        const int hi = static_cast<int>(__reduce_max_sync(0xffffffffu, max(max(bits[0], bits[1]), max(bits[2], bits[3]))) >> 23);
+        TileAsks ask = {half, 0u, before || hi + kFar <= run ? 1u : 0u, 0u};
+        before = false;
+        if (__any_sync(0xffffffffu, small)) {
+            const uint2 l = look(tile, n, lane);
+            f = l.x;
+            ask.with_f = l.y & 1u;
+            ask.eager |= ask.with_f;
+            ask.half = ask.with_f ? -1.f : half;
+            before = l.y != 0;
+        }
+        run = ask.eager ? hi : max(run, hi);
+        return ask;
+    }
+    // Looks at the latent codes of all tokens, 16 a lane.  Returns f, and whether f are to be used (1), whether all
+    // latents are small (2).
+    __device__ __noinline__ static uint2 look(const uint8_t* tile, int n, int lane) {
+        int f[4] = {0, 0, 0, 0}, g = kNoLatent;
+        const uint8_t* at = tile + (lane >> 3) * kBlock8Chunk + (lane & 7) * 16;
+#pragma unroll 4
+        for (int r = 0; r < n; ++r) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max_code16(*reinterpret_cast<const uint4*>(at + r * 128)));
+            const int e = top ? code_exp(top) : kNoLatent;
+            g = max(g, e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (4 * lane + k == r) f[k] = e;
+        }
+        uint32_t packed = 0;
+        bool use = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            use = use || (4 * lane + i < n && (f[i] <= g - kFar || f[i] == kNoLatent));
+            f[i] = 4 * lane + i >= n ? 0 : f[i] == kNoLatent ? static_cast<int>(kZeroF) : max(f[i] - g, -7);
+            packed |= static_cast<uint32_t>(f[i] & 0xFF) << (8 * i);
+        }
+        use = __any_sync(0xffffffffu, use);
+        return make_uint2(packed, (use ? 1u : 0u) | (g <= -kFar ? 2u : 0u));
+    }
+};
+
+constexpr float kLift = 48.f;
+struct RowPeak {  // of a row's piece: the y (rounded up) that the last first, up or eager move was for; the highest R
+    float peak, high;
+};
 template <int First, int Up, int Low>
 struct RowRef {
-    __device__ static bool is_up(float top, float R) { return top > R + 8.75f; }
+    // The common case, in one comparison: neither up nor low (nor f in use).
+    static constexpr float kMiddle = 0.5f * (kRoom - Low), kHalf = 0.5f * (kRoom + Low);
+    __device__ static bool stays(float top, float R, float half) { return !(fabsf(top - R - kMiddle) > half); }
+    __device__ static bool is_up(float top, float R, float room) { return top > R + room; }
     // (not for a unit with nothing visible, nor before the first)
     __device__ static bool is_low(float top, float R) {
         return top < R - static_cast<float>(Low) && top != __uint_as_float(kMinusInf);
     }
-    // The reference after a unit of tile n whose largest y is `top`; `same`: R has not changed since this warp's last unit,
-    // of tile n - 1.  `low` is the warp's for the row, `peak` the y (rounded up) that the row's last first or up move was for.
-    __device__ static float moved(float top, float R, bool same, uint32_t n, LowUnit& low, float& peak) {
-        if (is_up(top, R)) {
-            peak = ceilf(top);
-            return peak - (R == __uint_as_float(kMinusInf) ? First : Up);
+    // The reference after a piece's first unit (by itself: the code of all other moves is long, and seldom there when a piece
+    // starts).
+    __device__ static float first(float top, RowPeak& pk) {
+        if (top == __uint_as_float(kMinusInf)) return kNoRef;
+        pk.peak = ceilf(top);
+        return pk.high = pk.peak - First;
+    }
+    // The reference after a unit of tile n whose largest y + f is `top`; `same`: R has not changed since this warp's last
+    // unit, of tile n - 1.  `low` is the warp's for the row.
+    __device__ static float moved(float top, float R, bool same, uint32_t n, TileAsks ask, LowUnit& low, RowPeak& pk) {
+        const bool with_f = ask.with_f;
+        const int first_at = with_f ? 1 : First;
+        if (is_up(top, R, ask.room())) {
+            const bool first = R == kNoRef;
+            pk.peak = ceilf(top);
+            R = pk.peak - (first || with_f ? first_at : Up);
+            pk.high = first ? R : fmaxf(pk.high, R);
+        } else if (is_low(top, R)) {
+            if (ask.eager) {
+                pk.peak = ceilf(top);
+                R = fminf(R, fmaxf(pk.peak - first_at, pk.high - kLift));
+                low.at = kNoTile;
+            } else if (same && low.at == n - 1) {
+                R = fminf(R, fmaxf(ceilf(fmaxf(top, low.top)) - first_at, pk.peak - Up));
+                low.at = kNoTile;
+            } else {
+                low.top = top;
+                low.at = n;
+            }
         }
-        if (!is_low(top, R)) return R;
-        if (same && low.at == n - 1) {
-            low.at = kNoTile;
-            return fminf(R, fmaxf(ceilf(fmaxf(top, low.top)) - First, peak - Up));
-        }
-        low.top = top;
-        low.at = n;
         return R;
     }
 };
 // The exponent by which O and the sums are multiplied when R moves (<= -126: they vanish; 0 too where there was none).
 __device__ __forceinline__ int ref_exp(float from, float to) {
-    return from == __uint_as_float(kMinusInf) ? 0 : static_cast<int>(fmaxf(from - to, -127.f));
+    return from == kNoRef ? 0 : static_cast<int>(fmaxf(from - to, -127.f));
 }
 __device__ __forceinline__ float ref_factor(int d) { return d <= -126 ? 0.f : exp2_int(d); }
 // The factor from one reference to another (1 where there was none: the sum is then 0).
 __device__ __forceinline__ float ref_step(float from, float to) {
-    return from == __uint_as_float(kMinusInf) ? 1.f : ref_factor(static_cast<int>(fmaxf(from - to, -127.f)));
+    return from == kNoRef ? 1.f : ref_factor(static_cast<int>(fmaxf(from - to, -127.f)));
 }
-// What is added to y (0 where there is no reference yet: y is -inf then).
-__device__ __forceinline__ float ref_minus(float R) { return R == __uint_as_float(kMinusInf) ? 0.f : -R; }
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 operands (a_e5m2, b_e5m2: that one e5m2) and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false,
                                                     bool b_e5m2 = false) {
-    return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) | (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(b_mn_major) << 16) |
+    return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) |
+           (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(b_mn_major) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 

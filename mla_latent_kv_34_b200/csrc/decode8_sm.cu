@@ -17,9 +17,8 @@
 // maximum over a warp's tokens is a warp reduction, then the set's warps exchange them at one barrier and each decides on
 // the reference exponent (RowRef in decode8_common.cuh) by itself; the token's scale is one register.
 //
-// Warps: 0..7 softmax (set = warp / 4), 8 copies, 9 MMAs, 12..15 rescaling of O^T and a segment's output.  Scheduling and
-// output are the pair kernel's (decode8_tc.cu).  Every wait is bounded.
-#include <cuda.h>
+// Warps: 0..7 softmax (set = warp / 4), 8 copies, 9 MMAs, 10 what a tile's rows ask of the references (TileAsks), 12..15
+// rescaling of O^T and a segment's output.  Scheduling and output are the pair kernel's (decode8_tc.cu).  Every wait is bounded.
 #include <math_constants.h>
 
 #include "decode8_common.cuh"
@@ -32,7 +31,7 @@ using namespace d8;
 
 constexpr int kChunk = kBlock8Chunk;
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
-constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpEpi = 12;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpJudge = 10, kWarpEpi = 12;
 constexpr int kThreads = 512;
 
 constexpr uint32_t kNbSet = 1;  // named barriers 1, 2: the four softmax warps of a set
@@ -56,9 +55,12 @@ struct Lay {
     static constexpr int kOffRowF = kOffD + 2 * NR;          // [NR] fp32: 2^a scale log2 e
     static constexpr int kOffMax = kOffRowF + 4 * NR;        // [2 tiles][8 warps][kRN] row maxima
     static constexpr int kOffRef = kOffMax + 16 * kRN * 4;   // [8 warps][kRN] reference exponents, as the warp broadcasts them
-    static constexpr int kOffL = kOffRef + 8 * kRN * 4;      // [8 warps][kRN] (sum, reference) of a segment
-    static constexpr int kOffT = kOffL + 8 * kRN * 8;        // [8 warps][kRN] the second sum (not kStack)
-    static constexpr int kOffBar = kOffT + (kStack ? 0 : 8 * kRN * 4);
+    static constexpr int kOffL = kOffRef + 8 * kRN * 4;      // [8 warps][kRN] a segment's sums
+    static constexpr int kOffT = kOffL + 8 * kRN * 4;        // [8 warps][kRN] the second sums (not kStack)
+    static constexpr int kOffLR = kOffT + (kStack ? 0 : 8 * kRN * 4);  // [2 sets][kRN] its references
+    static constexpr int kOffF = kOffLR + 2 * kRN * 4;       // [4 tiles][128] f of the tokens (int8)
+    static constexpr int kOffAsk = kOffF + 4 * kTile;        // [4 tiles] TileAsks
+    static constexpr int kOffBar = kOffAsk + 4 * 16;
     static constexpr int kOffTail = kOffBar + kNumBars * 8;  // tmem base, abort flag, rescale place, [total, sequence, tile]
     static constexpr int kSmemBytes = kOffTail + 32;
     static_assert(2 * kN + 4 * kOC <= 512, "tensor memory");
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             mbar_init(&bars[kBEmpty + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[kBSFull + i], 1);
+            mbar_init(&bars[kBSFull + i], 2);  // the scores' MMAs and the judge
             mbar_init(&bars[kBSEmpty + i], kSoftThreads);
             mbar_init(&bars[kBPReady + i], kSoftThreads);
             mbar_init(&bars[kBPFree + i], 1);
@@ -391,8 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 lp[i] = 0.f;
                 if (!L::kStack) tp[i] = 0.f;
             }
+            // lane i < RN: row row0 + i's reference (rows of no query: one that makes P 0, and stays)
+            float R = lane < RN && row0 + lane < p.R ? kNoRef : -kNoRef;
             uint32_t sc = scale_bits(e0, s.t0);
-            float R = -CUDART_INF_F, peak = R;  // lane i < RN: row row0 + i's reference and peak
+            RowPeak peak = {R, R};
             LowUnit low = {0.f, kNoTile};
             const int lim0 = s.L - p.n_q + 1;  // keys below this are visible to every query of the step
             for (int t = s.t0; t < s.t1; ++t, ++n) {
@@ -427,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     for (int i = 0; i < RN; ++i)
                         if (tok >= lim0 + (row0 + i) / p.H) y[i] = -CUDART_INF_F;
                 }
+                const TileAsks& ask = reinterpret_cast<const TileAsks*>(smem + L::kOffAsk)[n & 3u];
                 // the tile's row maxima: lane i gets row row0 + i's over the warp's tokens, then over the set's
                 float top = -CUDART_INF_F;
 #pragma unroll
@@ -434,21 +439,31 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     const float v = warp_max_f32(y[i]);
                     if (lane == i) top = v;
                 }
+                float f = 0.f;
+                if (ask.with_f) {
+                    f = static_cast<float>(reinterpret_cast<const int8_t*>(smem + L::kOffF)[(n & 3u) * kTile + tk]);
+#pragma unroll
+                    for (int i = 0; i < RN; ++i) {
+                        if (f == kZeroF) y[i] -= kZeroDown;
+                        const float v = warp_max_f32(y[i] + f);
+                        if (lane == i) top = v;
+                    }
+                }
                 float* mx = reinterpret_cast<float*>(smem + L::kOffMax) + (8 * sb + 4 * set) * RN;
                 if (lane < RN) mx[qd * RN + lane] = top;
                 if (bar_red_or(kNbSet + set, 128, !ok || *abort_flag != 0)) {
                     ok = false;
                     break;
                 }
-                // (rows of no query keep R = -inf: P = 0)
                 if (lane < RN && row0 + lane < p.R)
                     top = fmaxf(fmaxf(mx[lane], mx[RN + lane]), fmaxf(mx[2 * RN + lane], mx[3 * RN + lane]));
-                else top = -CUDART_INF_F;
-                const uint32_t dither = dither0 ^ dither_mask(tk >> 4, t);
+                else top = R;
+                const uint32_t dither = dither0 + dither_mask(tk >> 4, t);
+                if (t == s.t0 && R == kNoRef) R = Ref::first(top, peak);
                 int d = 0;
-                if (__any_sync(0xffffffffu, Ref::is_up(top, R) || Ref::is_low(top, R))) {
+                if (!__all_sync(0xffffffffu, Ref::stays(top, R, ask.half))) {
                     const float was = R;
-                    R = Ref::moved(top, R, t > s.t0, n, low, peak);
+                    R = Ref::moved(top, R, t > s.t0, n, ask, low, peak);
                     d = ref_exp(was, R);
                 }
                 if (__any_sync(0xffffffffu, d != 0)) {
@@ -461,6 +476,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 }
                 if (lane < RN) refs[lane] = R;
                 __syncwarp();
+                if (f == kZeroF) {
+                    // a token whose latents are all zero: what the sums lack
+#pragma unroll
+                    for (int i = 0; i < RN; ++i) {
+                        const float a = ex2_approx(y[i] + kZeroDown - refs[i]) * inv_s;
+                        lp[i] += a;
+                        if (!L::kStack) tp[i] += a;
+                    }
+                }
+                __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
                 for (int i = 0; i < RN; i += 4) {
@@ -469,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     float v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        // a row without any visible token yet has R = -inf and y = -inf: P = 0
-                        v[k] = ex2_approx(Rs[k] == -CUDART_INF_F ? (y[i + k] != y[i + k] ? y[i + k] : -CUDART_INF_F) : y[i + k] - Rs[k]);
+                        v[k] = ex2_approx(y[i + k] - Rs[k]);  // (without any visible token yet: y = -inf, P = 0)
                         lp[i + k] = fmaf(v[k], inv_s, lp[i + k]);
                     }
                     if (L::kStack) {
@@ -519,14 +543,60 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 }
             }
             if (lane < RN) {
-                reinterpret_cast<float2*>(smem + L::kOffL)[warp * RN + lane] = make_float2(sum, R);
+                reinterpret_cast<float*>(smem + L::kOffL)[warp * RN + lane] = sum;
                 if (!L::kStack) reinterpret_cast<float*>(smem + L::kOffT)[warp * RN + lane] = tsum;
+                if (qd == 0) reinterpret_cast<float*>(smem + L::kOffLR)[row0 + lane] = R;  // (the set's warps have the same)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kBLReady]);
             ++kseg;
         }
         if (!ok) raise_abort(abort_flag, p.dev_status);
+    } else if (warp == kWarpJudge) {
+        // ---- what each tile asks of the references (TileAsks), ahead of the softmax, which is past tile n - 3 where it has read
+        //      the scores of tile n - 2.  A tile's codes stay until its aggregation, after the softmax.
+        SegWalk w = walk;
+        Seg s;
+        uint32_t n = 0;
+        bool ok = true;
+        TileJudge judge;
+        uint32_t next[4];
+        while (ok && w.next(p, s)) {
+            auto entry = [&](int t) { return t < s.t1 ? s.tab[t] : 0; };
+            auto load = [&](int t, int32_t e) {  // (a block's scales are there, whether of tokens or not)
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (t < s.t1) x = reinterpret_cast<const uint4*>(block_of(p, e, false) + kBlock8Scales)[lane];
+                next[0] = x.x; next[1] = x.y; next[2] = x.z; next[3] = x.w;
+            };
+            // the scales are asked for a tile ahead, the table entry two
+            load(s.t0, entry(s.t0));
+            int32_t e1 = entry(s.t0 + 1);
+            judge.reset();
+            for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                uint32_t bits[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bits[i] = next[i];
+                if (s.L - t * kTile < kTile) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) bits[i] = t * kTile + 4 * lane + i < s.L ? bits[i] : kNoScale;
+                }
+                load(t + 1, e1);
+                e1 = entry(t + 2);
+                const uint32_t sb = n & 1u, us = n >> 1;
+                ok = mbar_wait(&bars[kBFull + 2 * sb], us & 1u, abort_flag, kLimitNs) &&
+                     mbar_wait(&bars[kBFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint32_t f;
+                const TileAsks ask = judge.judge(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf, f);
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[kBSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs));
+                if (ask.with_f) reinterpret_cast<uint32_t*>(smem + L::kOffF)[(n & 3u) * (kTile / 4) + lane] = f;
+                if (lane == 0) reinterpret_cast<TileAsks*>(smem + L::kOffAsk)[n & 3u] = ask;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kBSFull + sb]);
+            }
+        }
+        if (!ok && lane == 0) raise_abort(abort_flag, p.dev_status);
     } else if (warp >= kWarpEpi) {
         // ---- rescaling and output: warps 12..15, lane = latent column 128 c + 32 qd + lane of block c
         const int qd = warp & 3;
@@ -600,15 +670,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             // R and the sums per row: the set's four warps ended with the same reference
             for (int r = 32 * qd + lane; r < p.R; r += 128) {
                 const int at = (r / RN) * 4 * RN + r % RN;
-                const float2* part = reinterpret_cast<const float2*>(smem + L::kOffL) + at;
-                const float2 a = part[0], b = part[RN], c = part[2 * RN], d = part[3 * RN];
-                const float l = (a.x + b.x) + (c.x + d.x);
+                const float* part = reinterpret_cast<const float*>(smem + L::kOffL) + at;
+                const float l = (part[0] + part[RN]) + (part[2 * RN] + part[3 * RN]);
+                const float ref = reinterpret_cast<const float*>(smem + L::kOffLR)[r];
                 float t = l;  // (the stacked lo term holds a bit more: one sum serves for both)
                 if (!L::kStack) {
                     const float* tp = reinterpret_cast<const float*>(smem + L::kOffT) + at;
                     t = (tp[0] + tp[RN]) + (tp[2 * RN] + tp[3 * RN]);
                 }
-                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float4(l != l ? 0.f : a.y, l, t, 0.f);
+                p.ml_part[static_cast<int64_t>(s.slot) * p.rs + r] = make_float4(l != l ? 0.f : ref, l, t, 0.f);
             }
             // the workspace holds [column / 32][row] x 32 fp32, rs rows per slot
             float* oseg = p.o_part + static_cast<int64_t>(s.slot) * p.rs * kDc;

@@ -29,10 +29,7 @@
 //
 // Every wait is bounded: on expiry the kernel records MLA_DEVERR_TIMEOUT, both CTAs of the pair abandon their loops,
 // let in-flight copies and MMAs land, free TMEM and return.
-#include <cuda.h>
 #include <math_constants.h>
-
-#include <mutex>
 
 #include "decode8_common.cuh"
 
@@ -67,13 +64,16 @@ constexpr int kSOffRing = 0;                           // two tiles
 constexpr int kSOffQR = 2 * kTileBytes;                // RoPE part of Q: [128 rows x (hi 64 | lo 64)] swizzled, 16 KB
 constexpr int kSOffStage = kSOffQR + kRows * 128;      // kStages staging buffers, kMsgStride apart
 constexpr int kScaleBufs = 4;
-constexpr int kScaleBytes = 2 * kTile * 2;             // a tile's token scales s, then log2 s, as bf16 (both exact)
+constexpr int kScaleInv = 2 * kTile * 2, kScaleF = 3 * kTile * 2, kScaleFlags = kScaleF + kTile;  // within a buffer
+constexpr int kScaleBytes = kScaleFlags + 16;          // a tile's token scales s, log2 s and 1 / s as bf16 (all exact), f as int8; TileAsks
 constexpr int kSOffScale = kSOffStage + kStages * kMsgStride;
 constexpr int kSOffRef = kSOffScale + kScaleBufs * kScaleBytes;  // [4][128] reference exponents handed on
 constexpr int kSOffLx = kSOffRef + 4 * kRows * 4;      // [3][3][128] a segment's two sums and R of the first three quarters
-constexpr int kSOffPeak = kSOffLx + 9 * kRows * 4;     // [128] a row's peak (RowRef)
-constexpr int kSOffLow = kSOffPeak + kRows * 4;        // [16 warps][32] LowUnit
-constexpr int kSOffBar = kSOffLow + kSoftWarps * 32 * 8;
+constexpr int kSOffPeak = kSOffLx + 9 * kRows * 4;     // [128] RowPeak
+constexpr int kSOffLow = kSOffPeak + kRows * 8;        // [16 warps][32] LowUnit
+constexpr int kNextBytes = 56;
+constexpr int kSOffNext = kSOffLow + kSoftWarps * 32 * 8;  // [2] NextSeg: a segment's, the one's before
+constexpr int kSOffBar = kSOffNext + 2 * kNextBytes;
 constexpr int kSBarFull = 0, kSBarEmpty = 4, kSBarSFull = 8, kSBarSEmpty = 10, kSBarPEmpty = 12,
               kSBarFree = kSBarPEmpty + kPSlots, kSBarStaged = kSBarFree + kStages, kSBarRef = kSBarStaged + kStages,
               kSBarQx = kSBarRef + 16, kSBarLx = kSBarQx + 4, kSBarQFree = kSBarLx + 4, kSBarQReady = kSBarQFree + 1,
@@ -106,6 +106,14 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, uint32_t p
 // before R moves (B 32, H 128, 8K: 124 us with 5 and 161 with 3, instead of 108).
 using Ref = RowRef<1, 6, 6>;
 
+// The softmax warps' next segment, looked up while they wait for the first scores and kept out of their registers.  (Each writes
+// the same; a warp that has begun a segment meets others still in the one before at most.)
+struct NextSeg {
+    Seg s;
+    SegWalk w;
+};
+static_assert(sizeof(NextSeg) == kNextBytes && kSOffNext % 8 == 0, "");
+
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float fmax16(const float (&v)[16]) {
     const float a = max3(v[0], v[1], v[2]), b = max3(v[3], v[4], v[5]), c = max3(v[6], v[7], v[8]);
@@ -135,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
         if (rank == 0) {
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&bars[kSBarFull + i], 1);
-                mbar_init(&bars[kSBarEmpty + i], 1);
+                mbar_init(&bars[kSBarEmpty + i], 2);  // the scores' MMAs and the judge
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bars[kSBarSFull + i], 2);  // the scores' MMAs and the scales
@@ -317,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             volatile float* lx = reinterpret_cast<volatile float*>(smem + kSOffLx) + 32 * qd + lane;
             uint64_t* bar_in = &bars[kSBarRef + 4 * ((cq + 3) & 3) + qd];
             uint64_t* bar_out = &bars[kSBarRef + 4 * cq + qd];
-            SegWalk w = walk, wn;
-            Seg s, sn;
+            SegWalk w = walk;
+            Seg s;
             uint32_t n = 0, kseg = 0, nref = 0;  // tiles, segments, references received
             // a row's state where its reference moves; both in shared memory, since moves are rare and registers are not
             LowUnit& low = reinterpret_cast<LowUnit*>(smem + kSOffLow)[32 * warp + lane];
-            float& peak = reinterpret_cast<float*>(smem + kSOffPeak)[r];
+            RowPeak& peak = reinterpret_cast<RowPeak*>(smem + kSOffPeak)[r];
             low.at = kNoTile;
             uint32_t stg = cq >> 1, stg_phase = 1;  // the staging buffer of message 2 n + cq / 2, and the phase it is free in
             bool ok = true;
@@ -432,28 +440,36 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 tc_fence_before();
                 mbar_arrive(&bars[kSBarQReady]);
                 // the next segment, whose queries are prefetched near the end of this one
-                wn = w;
-                const bool have_next = wn.next(p, sn);
-                const int t_pf = max(s.t0, s.t1 - 2);
-                const char* nq = (have_next && row_ok) ? reinterpret_cast<const char*>(
-                                                              p.q + (static_cast<int64_t>(sn.b) * p.R + rr) * kRow)
-                                                        : nullptr;
+                {
+                    NextSeg next{s, w};
+                    have = next.w.next(p, next.s);
+                    __syncwarp();
+                    if (lane == 0) *reinterpret_cast<NextSeg*>(smem + kSOffNext + (kseg & 1u) * kNextBytes) = next;
+                    __syncwarp();
+                }
+                const NextSeg* nx = reinterpret_cast<const NextSeg*>(smem + kSOffNext + (kseg & 1u) * kNextBytes);
+                const int t_pf = have && row_ok ? max(s.t0, s.t1 - 2) : -1;
                 // from here on a thread has rows rA = 32 qd + lane % 16 and rB = rA + 16, and 16 of the warp's columns: the
                 // tokens' scales are then read and unpacked once for two rows
                 const float rowfA = __shfl_sync(0xffffffffu, rowf, lane & 15), rowfB = __shfl_sync(0xffffffffu, rowf, 16 + (lane & 15));
                 const float2 fA = make_float2(rowfA, rowfA), fB = make_float2(rowfB, rowfB);
-                float RA = -CUDART_INF_F, RB = RA, R = RA;  // the references of rows rA, rB and 32 qd + lane
+                float RA = kNoRef, RB = kNoRef, R = kNoRef;  // the references of rows rA, rB and 32 qd + lane
                 float lA = 0.f, lB = 0.f, tA = 0.f, tB = 0.f;
-                const int limA = gA < p.R ? s.L - p.n_q + gA / p.H + 1 : 0;  // keys 0 .. lim-1 are visible
-                const int limB = gB < p.R ? s.L - p.n_q + gB / p.H + 1 : 0;
+                const int limA = gA < p.R ? s.L - p.n_q + gA / p.H + 1 : s.L;  // keys 0 .. lim-1 are visible
+                const int limB = gB < p.R ? s.L - p.n_q + gB / p.H + 1 : s.L;  // (rows of no query: zeros, not stored)
                 for (int t = s.t0; t < s.t1; ++t, ++n) {
                     const uint32_t sb = n & 1u, us = n >> 1;
-                    if (t == t_pf && have_next && row_ok)
-                        for (int c = cq; c < 9; c += 4) prefetch_l2(nq + 128 * c);
+                    if (t == t_pf)
+                        for (int c = cq; c < 9; c += 4)
+                            prefetch_l2(reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(nx->s.b) * p.R + rr) * kRow) + 128 * c);
                     const uint4* sw4 = reinterpret_cast<const uint4*>(smem + kSOffScale + (n % kScaleBufs) * kScaleBytes) + cb / 8;
                     ok = mbar_wait(&bars[kSBarSFull + sb], us & 1u, abort_flag, kLimitNs) && ok;
                     __syncwarp();
                     tc_fence_after();
+                    const TileAsks* ask =
+                        reinterpret_cast<const TileAsks*>(smem + kSOffScale + (n % kScaleBufs) * kScaleBytes + kScaleFlags);
+                    int d = 0;  // the exponent of the row's rescale
+                    uint32_t hiA[4], loA[4], hiB[4], loB[4];
                     float yA[16], yB[16];
                     {
                         uint32_t a[16], b[16];
@@ -497,19 +513,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 16));
                     mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 16));
                     // the reference: the previous unit's (another warp's), moved if this unit needs it, handed on
-                    const float lastA = RA, lastB = RB;
                     if (cq > 0 || t > s.t0) {
                         ok = mbar_wait(bar_in, nref & 1u, abort_flag, kLimitNs) && ok;
                         ++nref;
                         RA = ref_in[lane & 15];
                         RB = ref_in[16 + (lane & 15)];
                     }
-                    const float top = lane < 16 ? mA : mB;
+                    float top = lane < 16 ? mA : mB;
+                    float last = R;  // this warp's last unit's: the sums are relative to it
                     R = lane < 16 ? RA : RB;
-                    int d = 0;
-                    if (__any_sync(0xffffffffu, Ref::is_up(top, R) || Ref::is_low(top, R))) {
+                    if (t == s.t0) {  // (nothing in the sums yet)
+                        if (cq == 0) {
+                            R = Ref::first(top, peak);
+                            RA = __shfl_sync(0xffffffffu, R, lane & 15);
+                            RB = __shfl_sync(0xffffffffu, R, 16 + (lane & 15));
+                        }
+                        last = R;
+                    }
+                    if (!__all_sync(0xffffffffu, Ref::stays(top, R, ask->half))) {
+                        if (ask->with_f) {
+                            mA = mB = -CUDART_INF_F;
+                            const uint4 fw = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(sw4) - 2 * cb + kScaleF + cb);
+                            const uint32_t f4[4] = {fw.x, fw.y, fw.z, fw.w};
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float f = static_cast<float>(static_cast<int8_t>(f4[i / 4] >> (8 * (i % 4))));
+                                mA = fmaxf(mA, yA[i] + f);
+                                mB = fmaxf(mB, yB[i] + f);
+                            }
+                            mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 16));
+                            mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 16));
+                            top = lane < 16 ? mA : mB;
+                        }
                         const float was = R;
-                        R = Ref::moved(top, R, R == (lane < 16 ? lastA : lastB), n, low, peak);
+                        R = Ref::moved(top, R, R == last, n, *ask, low, peak);
                         d = ref_exp(was, R);
                         RA = __shfl_sync(0xffffffffu, R, lane & 15);
                         RB = __shfl_sync(0xffffffffu, R, 16 + (lane & 15));
@@ -518,26 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         ref_out[lane] = R;
                         mbar_arrive(bar_out);
                     }
-                    // the sums are relative to the reference of this warp's last unit
-                    if (__any_sync(0xffffffffu, lastA != RA || lastB != RB)) {
-                        const float a = ref_step(lastA, RA), b = ref_step(lastB, RB);
-                        lA *= a;
-                        tA *= a;
-                        lB *= b;
-                        tB *= b;
-                    }
-                    const float2 nA = make_float2(ref_minus(RA), ref_minus(RA)), nB = make_float2(ref_minus(RB), ref_minus(RB));
+                    const float2 nA = make_float2(-RA, -RA), nB = make_float2(-RB, -RB);
                     const uint32_t dm = dither_mask(cb >> 4, t);
                     float2 sA = make_float2(0.f, 0.f), sB = sA, rA = sA, rB = sA;
-                    uint32_t hiA[4], loA[4], hiB[4], loB[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint4 sw = sw4[k];
-                        const uint32_t ss[4] = {sw.x, sw.y, sw.z, sw.w};
+                        // 1 / s, as bf16 (2^kZeroDown / s for tokens whose latents are all zero)
+                        const uint4 sw = sw4[k + kScaleInv / 16];
+                        const uint32_t sb4[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {
                             const int c = 8 * k + 2 * i, o = c / 4;
-                            const float2 i0 = bf16x2_f32(0x7F007F00u - ss[i]), i1 = bf16x2_f32(0x7F007F00u - ss[i + 1]);  // 1 / s
+                            const float2 i0 = bf16x2_f32(sb4[i]), i1 = bf16x2_f32(sb4[i + 1]);
                             float2 a0 = add2(make_float2(yA[c], yA[c + 1]), nA), a1 = add2(make_float2(yA[c + 2], yA[c + 3]), nA);
                             a0 = make_float2(ex2_approx(a0.x), ex2_approx(a0.y));
                             a1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
@@ -548,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             a1 = bf16x2_f32(cvt_bf16x2(a1.x, a1.y));
                             rA = fma2(a0, i0, rA);
                             rA = fma2(a1, i1, rA);
-                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2) ^ dm, dither_pair(c / 2 + 1) ^ dm, hiA[o], loA[o]);
+                            split4_p(a0.x, a0.y, a1.x, a1.y, dither_pair(c / 2) + dm, dither_pair(c / 2 + 1) + dm, hiA[o], loA[o]);
                             float2 b0 = add2(make_float2(yB[c], yB[c + 1]), nB), b1 = add2(make_float2(yB[c + 2], yB[c + 3]), nB);
                             b0 = make_float2(ex2_approx(b0.x), ex2_approx(b0.y));
                             b1 = make_float2(ex2_approx(b1.x), ex2_approx(b1.y));
@@ -558,8 +587,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             b1 = bf16x2_f32(cvt_bf16x2(b1.x, b1.y));
                             rB = fma2(b0, i0, rB);
                             rB = fma2(b1, i1, rB);
-                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2) ^ dm, dither_pair(c / 2 + 1) ^ dm, hiB[o], loB[o]);
+                            split4_p(b0.x, b0.y, b1.x, b1.y, dither_pair(c / 2) + dm, dither_pair(c / 2 + 1) + dm, hiB[o], loB[o]);
                         }
+                    }
+                    if (__any_sync(0xffffffffu, R != last)) {
+                        const float step = ref_step(last, R);
+                        const float a = __shfl_sync(0xffffffffu, step, lane & 15);
+                        const float b = __shfl_sync(0xffffffffu, step, 16 + (lane & 15));
+                        lA *= a;
+                        tA *= a;
+                        lB *= b;
+                        tB *= b;
                     }
                     lA += sA.x + sA.y;
                     lB += sB.x + sB.y;
@@ -616,39 +654,76 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             make_float4(lt != lt ? 0.f : rmine, lt, tt, 0.f);
                 }
                 ++kseg;
-                w = wn;
-                s = sn;
-                have = have_next;
+                w = nx->w;
+                s = nx->s;
             }
             if (!ok) raise_abort(abort_flag, peer_abort, p.dev_status);
         } else if (warp == kWarpScale) {
-            // ---- scales: the 128 tokens' s = 2^k and k of each tile, two tiles ahead of the softmax.  The buffer of tile n
-            //      was tile n - 4's; a softmax warp that has read the scores of tile n - 2 is past tile n - 3.
+            // ---- scales: the 128 tokens' s = 2^k and k of each tile, ahead of the softmax, and what the tile asks of the
+            //      references (TileAsks).  The buffer of tile n was tile n - 4's; a softmax warp that has read the scores of
+            //      tile n - 2 is past tile n - 3.
             SegWalk w = walk;
             Seg s;
             uint32_t n = 0;
             bool ok = true;
+            TileJudge judge;
+            uint32_t next[4];
             while (ok && w.next(p, s)) {
+                auto entry = [&](int t) { return t < s.t1 ? s.tab[t] : 0; };
+                auto load = [&](int t, int32_t e) {  // (a block's scales are there, whether of tokens or not)
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (t < s.t1) x = reinterpret_cast<const uint4*>(block_of(p, e, false) + kBlock8Scales)[lane];
+                    next[0] = x.x; next[1] = x.y; next[2] = x.z; next[3] = x.w;
+                };
+                // the scales are asked for a tile ahead, the table entry two
+                load(s.t0, entry(s.t0));
+                int32_t e1 = entry(s.t0 + 1);
+                judge.reset();
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
-                    const uint32_t* src =
-                        reinterpret_cast<const uint32_t*>(block_of(p, s.tab[t], false) + kBlock8Scales) + 4 * lane;
                     uint32_t bits[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) bits[i] = t * kTile + 4 * lane + i < s.L ? src[i] : 0x3F800000u;
+                    for (int i = 0; i < 4; ++i) bits[i] = next[i];
+                    if (s.L - t * kTile < kTile) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) bits[i] = t * kTile + 4 * lane + i < s.L ? bits[i] : kNoScale;
+                    }
+                    load(t + 1, e1);
+                    e1 = entry(t + 2);
                     const uint32_t sb = n & 1u, us = n >> 1;
+                    ok = mbar_wait(&bars[kSBarFull + 2 * sb], us & 1u, abort_flag, kLimitNs) &&
+                         mbar_wait(&bars[kSBarFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint32_t f;
+                    const TileAsks ask =
+                        judge.judge(smem + kSOffRing + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf, f);
+                    if (lane < 2) mbar_arrive(&bars[kSBarEmpty + 2 * sb + lane]);
                     ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
-                    uint2 sc, ex;
                     uint32_t e[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        e[i] = __float_as_uint(static_cast<float>(static_cast<int>(bits[i] >> 23) - 127));
-                    sc.x = __byte_perm(bits[0], bits[1], 0x7632);
-                    sc.y = __byte_perm(bits[2], bits[3], 0x7632);
-                    ex.x = __byte_perm(e[0], e[1], 0x7632);
-                    ex.y = __byte_perm(e[2], e[3], 0x7632);
+                    for (int i = 0; i < 4; ++i) e[i] = __float_as_uint(static_cast<float>(static_cast<int>(bits[i] >> 23) - 127));
                     uint8_t* to = smem + kSOffScale + (n % kScaleBufs) * kScaleBytes + 8 * lane;
+                    const uint2 sc = make_uint2(__byte_perm(bits[0], bits[1], 0x7632), __byte_perm(bits[2], bits[3], 0x7632));
+                    uint2 is = make_uint2(0x7F007F00u - sc.x, 0x7F007F00u - sc.y);
+                    if (ask.with_f) {
+                        uint32_t up[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            up[i] = 0;
+                            if (static_cast<int8_t>(f >> (8 * i)) == static_cast<int>(kZeroF)) {
+                                e[i] = __float_as_uint(__uint_as_float(e[i]) - kZeroDown);
+                                up[i] = static_cast<uint32_t>(kZeroDown) << 7;
+                            }
+                        }
+                        is.x += up[0] | (up[1] << 16);
+                        is.y += up[2] | (up[3] << 16);
+                        *reinterpret_cast<uint32_t*>(to - 4 * lane + kScaleF) = f;
+                    }
                     *reinterpret_cast<uint2*>(to) = sc;
-                    *reinterpret_cast<uint2*>(to + 2 * kTile) = ex;
+                    *reinterpret_cast<uint2*>(to + 2 * kTile) =
+                        make_uint2(__byte_perm(e[0], e[1], 0x7632), __byte_perm(e[2], e[3], 0x7632));
+                    *reinterpret_cast<uint2*>(to + kScaleInv) = is;
+                    if (lane == 0) *reinterpret_cast<TileAsks*>(to + kScaleFlags) = ask;
                     ok = __all_sync(0xffffffffu, ok);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars[kSBarSFull + sb]);

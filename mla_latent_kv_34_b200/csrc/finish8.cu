@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
         while (2 * S * n <= kWarps) S *= 2;
         const int k = warp % S;
         float2 acc[8];
-        float M = -CUDART_INF_F, z = 0.f, zt = 0.f;
+        float M = kNoRef, z = 0.f, zt = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] = make_float2(0.f, 0.f);
         auto write_row = [&](int i) {  // row i's o into the B operand, its lse out
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
             int row[kBatch];  // the row that item ends, or -1
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                ml[u] = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+                ml[u] = make_float4(kNoRef, 0.f, 0.f, 0.f);
                 row[u] = -1;
                 if (i < n) {
                     const Row w = tab[i];
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                if (ml[u].x != -CUDART_INF_F) {
+                if (ml[u].x != kNoRef) {
                     if (ml[u].x > M) {
                         const float sc = ref_step(M, ml[u].x);
                         M = ml[u].x;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) finish8_kernel(const __grid_const
                 }
                 if (S == 1 && row[u] >= 0) {
                     write_row(row[u]);
-                    M = -CUDART_INF_F;
+                    M = kNoRef;
                     z = zt = 0.f;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) acc[q] = make_float2(0.f, 0.f);

@@ -9,16 +9,40 @@ that its sum shows in the output.
 import numpy as np
 import pytest
 
-from cache8_cases import bf16_values, peaked_queries, peaked_rows
-from test_gpu_cache8 import Problem8
+from cache8_cases import L2, U, bf16_values, peaked_queries, peaked_rows
+from gpu_harness import to_dev_bf16
+from oracle import cache8 as o8
+from test_gpu_cache8 import SCALE, Problem8, bf16_to_f64, f32_to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 
 
 def check(p, **kw):
+    """Problem8.check's tolerances with one more term in a score's error d, for queries with a few large elements.
+
+    A query row is scaled by a power of two so that its largest element lies in (224, 448] and held by two e4m3 terms,
+    whose step is 2^-9 at the least: an element of eight significant bits is exact down to 2^-2, below that off by half a step,
+    2^-10, which is at most 2^-10 / 224 of the row's largest.  So d grows by max |q| * 2^-10 / 224 times the sum of
+    |c_ti| over the columns i of those elements, times the softmax scale.
+    """
     out, lse = p.decode(**kw)
     assert p.status.item() == 0
-    p.check(out, lse)
+    out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    W, e2, r2 = bf16_to_f64(p.W_bits), 0.0, 0.0
+    for b in range(p.B):
+        rows = slice(b * p.n_q, (b + 1) * p.n_q)
+        q = bf16_to_f64(p.q_bits[rows])
+        ref, ref_lse, _, A, reach = o8.attend(p.rows[b], q, W, p.n_q, SCALE)
+        top = np.abs(q).max(-1)
+        small = (np.abs(q) < top[..., None] * (0.25 / 224)).astype(np.float64)
+        d = 577 * 2.0 ** -23 * reach + top * (2.0 ** -10 / 224) * SCALE * (small @ np.abs(p.rows[b]).T).max(-1)
+        err = (2 * U + 2 * d[..., None] + 2.0 ** -14) * A
+        tol = np.einsum("jhc,hdc->jhd", err, np.abs(W)) + U * np.abs(ref) * (1 + 2.0 ** -7) + 2.0 ** -20
+        assert np.isfinite(out[rows]).all() and np.isfinite(lse[rows]).all(), b
+        assert (np.abs(out[rows] - ref) <= tol).all(), (b, (np.abs(out[rows] - ref) - tol).max())
+        assert (np.abs(lse[rows] - ref_lse) <= d + 2.0 ** -13).all(), (b, np.abs(lse[rows] - ref_lse).max())
+        e2, r2 = e2 + ((out[rows] - ref) ** 2).sum(), r2 + (ref ** 2).sum()
+    assert np.sqrt(e2 / r2) <= L2, np.sqrt(e2 / r2)
 
 
 def peaked(n, H, n_q=1, lengths=None, **kw):
@@ -75,3 +99,85 @@ def test_decode8_peaks_one_after_another(H):
             return y
         check(Problem8([6000], H, 1, rows=lambda b, x: bf16_values(rows(b, x)), q=lambda v: peaked_queries(v.shape[:-1])),
               num_splits=1)
+
+
+# ------------------------------------------------------------------ scales that differ
+
+def scaled_up(p, k):
+    """W^UV times 2^k, so that outputs of small rows are not below the tolerances' absolute term."""
+    p.W_bits = f32_to_bf16_bits(bf16_to_f64(p.W_bits) * 2.0 ** k)
+    p.W = to_dev_bf16(p.W_bits, "cuda")
+    return p
+
+
+def small_rows(n, a, seed=0):
+    rng = np.random.default_rng(seed)
+    x = a * rng.standard_normal((n, 576))
+    x[:, :512] += 0.5 * a * rng.standard_normal(512)
+    return x
+
+
+ZEROS = {"first": [0], "mid_tile": [70], "later_tile": [300], "last": [510], "some": list(range(3, 511, 37)),
+         "a_tile": list(range(128, 256)), "prefix": list(range(200)), "unit": list(range(160, 192))}
+
+
+@pytest.mark.parametrize("H", [16, 24, 40, 128])
+@pytest.mark.parametrize("a", [1e-1, 1e-2, 4e-3, 3e-4, 1e-5, 1e-8])
+def test_decode8_rows_of_zeros_among_small_ones(H, a):
+    """A row of zeros has scale 1 and adds nothing to o; the others' scales go down to 2^-33."""
+    for where in ZEROS.values():
+        def rows(b, x):
+            y = bf16_values(small_rows(len(x), a))
+            y[where] = 0.0
+            return y
+        p = Problem8([511], H, 1, rows=rows, q=lambda v: 0.5 * v / a)
+        check(scaled_up(p, -round(np.log2(a))), num_splits=1)
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+@pytest.mark.parametrize("gap", [4.0, 12.0, 20.0])
+def test_decode8_token_without_latents(H, gap):
+    """A token whose latents are all zero and whose RoPE columns carry a score far above the others': it scales the
+    output down and adds nothing to it."""
+    for at in (0, 200):
+        def rows(b, x):
+            y = small_rows(len(x), 1.0)
+            y[:, 512:] = 0.0
+            y[at, :512] = 0.0
+            y[at, 575] = gap / 8.0
+            return bf16_values(y)
+        p = Problem8([700], H, 1, rows=rows, q=lambda v: peaked_queries(v.shape[:-1]))
+        check(scaled_up(p, round(gap * 1.4427)), num_splits=1)
+
+
+@pytest.mark.parametrize("H", [16, 24, 40, 128])
+@pytest.mark.parametrize("ratio", [16.0, 64.0, 1024.0])
+def test_decode8_tail_behind_a_peak_of_large_scale(H, ratio):
+    """The peak's scale is far above the tail's by its RoPE columns alone."""
+    for at in (0, 1500):
+        for mass in (0.05, 0.5):
+            check(peaked(8000, H, mass=mass, at=at, ratio=ratio), num_splits=1)
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+@pytest.mark.parametrize("ratio", [32.0, 2000.0])
+def test_decode8_scales_that_fall_along_the_sequence(H, ratio):
+    """Whole tiles whose RoPE columns set a large scale, then tiles without, and back."""
+    def rows(b, x):
+        y = small_rows(len(x), 1.0)
+        y[:, 512:575] = 0.0
+        y[:, 575] *= 0.1
+        y[:300, 574] = y[700:900, 574] = ratio
+        return bf16_values(y)
+    check(Problem8([1500], H, 1, rows=rows, q=lambda v: peaked_queries(v.shape[:-1])), num_splits=1)
+    check(Problem8([1500, 290, 800], H, 2, rows=rows, q=lambda v: peaked_queries(v.shape[:-1])), num_splits=2)
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+def test_decode8_every_row_of_another_scale(H):
+    """Amplitudes spread over 2^-12 .. 2^12 within every tile; the latents' mean goes with them."""
+    def rows(b, x):
+        y = small_rows(len(x), 1.0) * 2.0 ** np.random.default_rng(5).uniform(-12, 12, (len(x), 1))
+        y[:, 512:] = 0.0
+        return bf16_values(y)
+    check(Problem8([600], H, 1, rows=rows, q=lambda v: 1e-5 * v), num_splits=1)
