@@ -286,7 +286,8 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
  * nothing.  Beside a token whose k^R is 2^4 to 2^8 times its latent values the
  * others of its 32 (128) have up to that much less.  What lies 2^-48 below the
  * largest is lost.  A NaN among a row's visible tokens, or a NaN or infinity in
- * its query, makes its out and lse NaN.
+ * its query, makes its out and lse NaN; one in a later token of the step, which
+ * the row does not see, does not reach it.
  */
 size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits);
 mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks,

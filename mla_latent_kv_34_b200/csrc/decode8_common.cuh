@@ -289,6 +289,38 @@ __device__ __forceinline__ uint32_t max_code16(uint4 x) {
     }
     return max((m >> 8) & 0x7Fu, m >> 24);
 }
+// 16 codes with 0 for NaN, in place: a token that some query of the step does not see has P = 0 there, and 0 * NaN would
+// reach it; the queries that see it have a NaN score.
+__device__ __forceinline__ void nan_to_zero16(uint8_t* at) {
+    uint4 x = *reinterpret_cast<const uint4*>(at);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w}, any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t n = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the top bit of each byte that is NaN
+        any |= n;
+        w[i] &= ~((n >> 7) * 0xFFu);
+    }
+    if (any) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// For rows first .. last - 1 of a tile, by a warp; for one row, by a thread.  (Not inlined: seldom needed, and the loops that call
+// them fill the instruction cache.)
+static __device__ __noinline__ void nan_to_zero_rows(uint8_t* tile, int first, int last, int lane) {
+    uint8_t* at = tile + (lane >> 3) * kBlock8Chunk + (lane & 7) * 16;
+    uint32_t any = 0;
+#pragma unroll 8
+    for (int r = first; r < last; ++r) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + r * 128);
+        any |= ((x.x & 0x7F7F7F7Fu) + 0x01010101u) | ((x.y & 0x7F7F7F7Fu) + 0x01010101u) | ((x.z & 0x7F7F7F7Fu) + 0x01010101u) |
+               ((x.w & 0x7F7F7F7Fu) + 0x01010101u);
+    }
+    if ((any & 0x80808080u) == 0) return;
+    for (int r = first; r < last; ++r) nan_to_zero16(at + r * 128);
+}
+static __device__ __noinline__ void nan_to_zero_row(uint8_t* row) {
+#pragma unroll 1
+    for (int u = 0; u < 32; ++u) nan_to_zero16(row + (u >> 3) * kBlock8Chunk + (u & 7) * 16);
+}
+
 // One warp judges the tiles of a segment one after another, from the codes that the copies brought to shared memory.  (The
 // code of the common case is kept short: the loops of a block's warps share an instruction cache that they fill.)
 struct TileJudge {

@@ -427,6 +427,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
 #pragma unroll
                 for (int i = 0; i < RN; ++i) y[i] = fmaf(y[i] * st, rowf[i], et);
                 if (tok >= lim0) {
+                    bool bad = false;  // a token that not every query sees: NaN made 0 in V (its scores are NaN, and formed)
+#pragma unroll
+                    for (int i = 0; i < RN; ++i) bad = bad || y[i] != y[i];
+                    if (bad && set == 0 && tok < s.L) {
+                        ok = mbar_wait(&bars[kBFull + 2 * sb], us & 1u, abort_flag, kLimitNs) &&
+                             mbar_wait(&bars[kBFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs) && ok;
+                        nan_to_zero_row(smem + L::kOffRing + sb * kTileBytes + tk * 128);
+                    }
 #pragma unroll
                     for (int i = 0; i < RN; ++i)
                         if (tok >= lim0 + (row0 + i) / p.H) y[i] = -CUDART_INF_F;

@@ -823,15 +823,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         }
                         ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
-                        if (h == 0 && nvalid < kTile) {
-                            // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN)
+                        // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN); rows that not every query sees:
+                        // NaN made 0
+                        const int some = max(0, s.L - p.n_q + 1 - t * kTile);
+                        if (h == 0 && some < kTile) {
+                            uint8_t* v = smem + kOOffV + st * kVBytes;
+                            if (some < nvalid) {
+                                ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
+                                nan_to_zero_rows(v, some, nvalid, lane);
+                            }
                             const int nz = (kTile - nvalid) * 8;  // 16-byte units per chunk
                             for (int i = lane; i < 4 * nz; i += 32) {
                                 const int c = i / nz, q = i % nz;
-                                *reinterpret_cast<uint4*>(smem + kOOffV + st * kVBytes + c * kChunk + nvalid * 128 + q * 16) =
-                                    make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(v + c * kChunk + nvalid * 128 + q * 16) = make_uint4(0, 0, 0, 0);
                             }
                             fence_proxy_async_cta();
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
                         }
                         // (read by every lane: which of the two units move some row's reference)
                         const uint32_t* moved = reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes);

@@ -8,6 +8,7 @@ that its sum shows in the output.
 
 import numpy as np
 import pytest
+import torch
 
 from cache8_cases import L2, U, bf16_values, peaked_queries, peaked_rows
 from gpu_harness import to_dev_bf16
@@ -181,3 +182,50 @@ def test_decode8_every_row_of_another_scale(H):
         y[:, 512:] = 0.0
         return bf16_values(y)
     check(Problem8([600], H, 1, rows=rows, q=lambda v: 1e-5 * v), num_splits=1)
+
+
+# ------------------------------------------------------------------ NaN in tokens that some queries see
+
+@pytest.mark.parametrize("H,n_q,lengths,at", [
+    (16, 2, [200, 150, 130], -1), (16, 3, [129, 128, 300], -2), (12, 3, [64, 300, 257], -1), (11, 4, [5, 4, 200], -3),
+    (128, 2, [200, 150, 130], -1), (64, 3, [129, 128, 300], -2), (128, 3, [3, 4, 700], -1), (20, 40, [300, 41, 129], -17),
+    (128, 256, [257, 300], -200), (1, 40, [40, 300], -1)])
+def test_decode8_nan_in_a_token_of_the_step(H, n_q, lengths, at):
+    """A NaN (or infinity) in one of the step's tokens: the queries from that token on are NaN, all of them; the ones before,
+    and the other sequences, are what they are without it."""
+    b = 1
+    bad = lengths[b] + at
+
+    def rows(i, x):
+        x = bf16_values(x)
+        if i == b:
+            x[bad, 3], x[bad, 300] = np.inf, np.nan
+        return x
+    p = Problem8(lengths, H, n_q, rows=rows)
+    out, lse = p.decode()
+    first = n_q + at        # the first query that sees the token
+    assert p.status.item() == 0
+    assert torch.isnan(out[b * n_q + first:(b + 1) * n_q]).all() and torch.isnan(lse[b * n_q + first:(b + 1) * n_q]).all()
+    p.check(out, lse, seqs=[i for i in range(p.B) if i != b], l2=False)
+    # the queries before it: a sequence that ends before the token, with n_q + at queries
+    if first > 0:
+        ref, ref_lse, _, A, reach = o8.attend(p.rows[b][:bad], bf16_to_f64(p.q_bits[b * n_q:b * n_q + first]),
+                                              bf16_to_f64(p.W_bits), first, SCALE)
+        got = out[b * n_q:b * n_q + first].float().cpu().numpy().astype(np.float64)
+        d = 577 * 2.0 ** -23 * reach
+        tol = np.einsum("jhc,hdc->jhd", (2 * U + 2 * d[..., None] + 2.0 ** -14) * A, np.abs(bf16_to_f64(p.W_bits)))
+        assert (np.abs(got - ref) <= tol + U * np.abs(ref) * (1 + 2.0 ** -7) + 2.0 ** -20).all()
+        assert (np.abs(lse[b * n_q:b * n_q + first].cpu().numpy() - ref_lse) <= d + 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+def test_decode8_visible_nan_makes_all_of_a_row_nan(H):
+    def rows(b, x):
+        x = bf16_values(x)
+        if b == 1:
+            x[7, 575] = np.nan
+        return x
+    p = Problem8([200, 150, 130], H, 1, rows=rows)
+    out, lse = p.decode()
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    p.check(out, lse, seqs=[0, 2])
