@@ -273,7 +273,9 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
  *   cache8     pool of cap_blocks blocks of MLA_BLOCK8_BYTES, written by
  *              mla_append_cache8 (a token's scale has to be a power of two;
  *              bytes of no token are never used)
- *   workspace  of at least mla_decode8_workspace_bytes() bytes
+ *   workspace  of at least mla_decode8_workspace_bytes() bytes (0 for shapes
+ *              that the call refuses and for B = 0; so with the other two
+ *              decode calls' size functions, but for B = 0 of mla_decode)
  * Scores are formed from the bf16 query and the codes without a further
  * rounding of either (query elements below 2^-9 of their row's largest are
  * held to 2^-17 of it); their sums, the softmax and its sums are fp32.  In the

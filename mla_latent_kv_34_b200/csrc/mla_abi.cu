@@ -121,6 +121,9 @@ mla_status check_decode_shape(int B, int64_t cap_blocks, int max_blocks, int n_q
     return MLA_OK;
 }
 
+// Whether the size functions give a size: shapes that the calls refuse have none (and would overflow on the way to one).
+bool has_size(int B, int n_q, int H, int num_splits) { return check_decode_shape(B, 1, 1, n_q, H, num_splits) == MLA_OK; }
+
 }  // namespace
 
 extern "C" {
@@ -257,7 +260,7 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
 }
 
 size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits) {
-    if (B < 1 || n_q < 1 || H < 1 || num_splits < 0) return 0;
+    if (B == 0 || !has_size(B, n_q, H, num_splits)) return 0;
     return ws8_layout(B, n_q, H).total;
 }
 
@@ -294,7 +297,7 @@ mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks, co
 }
 
 size_t mla_decode_workspace_bytes(int B, int n_q, int H, int num_splits) {
-    if (B < 0 || n_q < 1 || H < 1 || num_splits < 0) return 0;
+    if (!has_size(B, n_q, H, num_splits)) return 0;
     return tc_ws_layout(B, n_q, H).total;
 }
 
@@ -365,7 +368,7 @@ mla_status mla_decode(const void* q, const void* cache, int64_t cap_blocks, cons
 }
 
 size_t mla_decode_cudacore_workspace_bytes(int B, int n_q, int H, int num_splits) {
-    if (B < 0 || n_q < 1 || H < 1 || num_splits < 0) return 0;
+    if (B == 0 || !has_size(B, n_q, H, num_splits)) return 0;
     const int S = num_splits ? num_splits : auto_splits(B, n_q, H);
     return decode_ws_layout(B, n_q, H, S).total;
 }

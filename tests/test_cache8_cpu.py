@@ -133,3 +133,20 @@ def test_peaked_cases_show_a_lost_tail(mass):
     assert np.abs(np.log(p[:, 1:].sum(1) / mass)).max() < 1.1
     lost = np.einsum("hc,hdc->hd", p[:, :1] * rows[0, :512], W)
     assert np.linalg.norm(lost - out[0]) > 1.5 * L2 * np.linalg.norm(out)
+
+
+@pytest.mark.parametrize("name", ["mla_decode8_workspace_bytes", "mla_decode_workspace_bytes",
+                                  "mla_decode_cudacore_workspace_bytes"])
+def test_workspace_sizes_of_refused_shapes(mla, name):
+    """Shapes that the calls refuse have size 0: no overflow, no division by zero (n_q * H = 2^32, B = 0 of an automatic
+    split), which ended the process."""
+    size = getattr(mla.lib, name)
+    top = (1 << 31) - 1
+    for B, n_q, H, splits in ((1, 1 << 16, 1 << 16, 0), (1, 257, 16, 0), (1, 1, 129, 0), (1, 0, 16, 0), (1, 1, 0, 0),
+                              (-1, 1, 16, 0), (1, 1, 16, -1), (1, 1, 16, 257), (top, 256, 128, 0), (top, top, top, 3),
+                              (1 << 24, 1, 1, 0), (1 << 16, 1 << 15, 1, 0)):
+        assert size(B, n_q, H, splits) == 0, (B, n_q, H, splits)
+    assert size(0, 1, 16, 0) == 0 or name == "mla_decode_workspace_bytes"
+    assert size(0, 1, 16, 2) == 0 or name == "mla_decode_workspace_bytes"
+    for B, n_q, H in ((1, 1, 1), (1, 256, 128), (65535, 256, 1), (4096, 2, 128)):
+        assert size(B, n_q, H, 0) >= B * n_q * H * 2048, (B, n_q, H)
