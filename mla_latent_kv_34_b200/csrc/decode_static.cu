@@ -63,6 +63,7 @@ extern "C" mla_status mla_decode_static(const void* q, const void* cache, int64_
     const size_t need = mla_decode_workspace_bytes(B, n_q, H, num_splits);
     if (need > static_cast<size_t>(MLA_DECODE_STATIC_SCRATCH_BYTES)) return MLA_ERR_WORKSPACE;
     if (B == 0) return MLA_OK;
+    if (need == 0) return MLA_ERR_UNSUPPORTED_SHAPE;  // (a shape that mla_decode refuses)
     // argument errors are reported before the device is touched, as for every other entry point
     if (!q || !cache || !block_table || !kv_len || !W_UV || !out) return MLA_ERR_INVALID_ARG;
     void* scratch = nullptr;

@@ -150,3 +150,9 @@ def test_workspace_sizes_of_refused_shapes(mla, name):
     assert size(0, 1, 16, 2) == 0 or name == "mla_decode_workspace_bytes"
     for B, n_q, H in ((1, 1, 1), (1, 256, 128), (65535, 256, 1), (4096, 2, 128)):
         assert size(B, n_q, H, 0) >= B * n_q * H * 2048, (B, n_q, H)
+
+
+def test_static_decode_refuses_shapes_before_the_device(mla):
+    f = ctypes.c_void_p(4096)
+    for B, n_q, H, splits in ((1, 1, 129, 0), (1, 257, 16, 0), (1, 1, 16, 257), (1 << 24, 1, 1, 0)):
+        assert mla.lib.mla_decode_static(f, f, 10, f, 4, f, f, B, n_q, H, 0.07, splits, f, None, None, None) == 2
