@@ -45,7 +45,6 @@ __host__ __device__ __forceinline__ int block_offset(int r, int c) {
     return (c >> 6) * kBlockChunk + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
 }
 
-
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
     return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }

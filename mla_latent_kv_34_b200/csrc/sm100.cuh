@@ -390,8 +390,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
-// 16 lanes x 16 + 16 consecutive 32-bit columns: threads 0..15 get lanes (base lane + i), columns col..col+15, threads
-// 8 columns of this warp's 32 lanes.
+// 32 lanes x 8 consecutive 32-bit columns, read and written.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -403,6 +402,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                  : "memory");
 }
 
+// 16 lanes x 16 + 16 consecutive 32-bit columns: threads 0..15 get lanes (base lane + i), columns col..col+15, threads
 // 16..31 the same lanes, columns col+16..col+31.
 __device__ __forceinline__ void tmem_ld16_halves(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

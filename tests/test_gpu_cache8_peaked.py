@@ -229,3 +229,11 @@ def test_decode8_visible_nan_makes_all_of_a_row_nan(H):
     out, lse = p.decode()
     assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
     p.check(out, lse, seqs=[0, 2])
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+@pytest.mark.parametrize("a", [2.0 ** -32, 2.0 ** -41, 2.0 ** -46])
+def test_decode8_rows_at_the_smallest_scale(H, a):
+    """Rows whose scale is 2^-40, the least there is, and queries as large; W^UV brings the output back to the order of 1."""
+    p = Problem8([300, 70], H, 1, rows=lambda b, x: bf16_values(small_rows(len(x), a, seed=b)), q=lambda v: 0.5 * v / a)
+    check(scaled_up(p, -round(np.log2(a))), num_splits=1)
