@@ -202,9 +202,10 @@ __device__ __forceinline__ void split4_p(float p0, float p1, float p2, float p3,
     hi = a | (static_cast<uint32_t>(b) << 16);
     lo = __byte_perm(d01 + dither01, d23 + dither23, 0x7531);
 }
-// The same, for any p, with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant bits down
-// to 2^-10 and steps of 2^-13 below.  With the one bit more, a dithered rounding (`dither`: seven bits for each half) of
-// every probability still holds it within 2^-8.  An e4m3 code of x has the bits of the fp16 of 2^-8 x, less its top exponent bit and its last seven.
+// The same, for any p, with lo * 2^4 in e4m3, for accumulators that keep the lo part in columns of their own: 4 significant
+// bits down to 2^-10 and steps of 2^-13 below.  With the one bit more, a dithered rounding (`dither`: seven bits for each half)
+// of a probability down to 2^-5 still holds it within 2^-8.  An e4m3 code of x has the bits of the fp16 of 2^-8 x, less its top
+// exponent bit and its last seven.
 __device__ __forceinline__ void split4_p16(float p0, float p1, float p2, float p3, uint32_t dither, uint32_t& hi,
                                            uint32_t& lo) {
     uint32_t h01, h23, d01, d23;
@@ -272,22 +273,25 @@ struct TileAsks {
     uint32_t with_f, eager, pad;
     __device__ __forceinline__ float room() const { return with_f ? kRoomF : kRoom; }
 };
-// f of a token whose largest latent code (sign dropped) is `top`.
-__device__ __forceinline__ int code_exp(uint32_t top) {  // (0x7E is 448)
-    return min(static_cast<int>(top >> 3) - 15 + ((top & 7u) == 7u ? 1 : 0), 0);
-}
 constexpr int kNoLatent = -99;
 constexpr uint32_t kNoScale = 0x0D800000u;  // 2^-100, for tokens that do not exist (their scores are masked)
-// The largest of 16 codes, signs dropped.
-__device__ __forceinline__ uint32_t max_code16(uint4 x) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// The exponent of a token's largest latent code against 448 (kNoLatent: all are zero), by one thread of a warp that takes
+// 32 rows in order: `row` is the token's, r its index.
+__device__ __forceinline__ int latent_exp(const uint8_t* row, int r) {
     uint32_t m = 0;
+#pragma unroll 8
+    for (int u = 0; u < 32; ++u) {  // (each lane its own unit of a column block: no two of eight lanes meet in a bank)
+        const uint4 x = *reinterpret_cast<const uint4*>(row + (u >> 3) * kBlock8Chunk + (((u + r) & 7) << 4));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m = __vmaxu2(m, w[i] & 0x7F007F00u);
-        m = __vmaxu2(m, (w[i] << 8) & 0x7F007F00u);
+        for (int i = 0; i < 4; ++i) {
+            m = __vmaxu2(m, w[i] & 0x7F007F00u);
+            m = __vmaxu2(m, (w[i] << 8) & 0x7F007F00u);
+        }
     }
-    return max((m >> 8) & 0x7Fu, m >> 24);
+    const uint32_t top = max((m >> 8) & 0x7Fu, m >> 24);
+    // (0x7E is 448)
+    return top == 0 ? kNoLatent : min(static_cast<int>(top >> 3) - 15 + ((top & 7u) == 7u ? 1 : 0), 0);
 }
 // 16 codes with 0 for NaN, in place: a token that some query of the step does not see has P = 0 there, and 0 * NaN would
 // reach it; the queries that see it have a NaN score.
@@ -331,54 +335,53 @@ struct TileJudge {
         before = false;
     }
     // The tile's codes are at `tile`, its first n >= 1 tokens exist; `bits`: the scales of tokens 4 lane .. 4 lane + 3 (kNoScale for
-    // those that do not).  f of those, as described, four int8, where they are in use.
-    __device__ __forceinline__ TileAsks judge(const uint8_t* tile, int n, const uint32_t (&bits)[4], int lane, float half, uint32_t& f) {
+    // those that do not).  Where f are in use, the tokens' go to `fs` (int8, in shared memory).
+    __device__ __forceinline__ TileAsks judge(const uint8_t* tile, int n, const uint32_t (&bits)[4], int lane, float half, int8_t* fs) {
         // 16 codes of a token, none of which is 2 = 448 * 2^-7.8 or more: the upper exponent bit is not set
         const uint8_t* at = tile + lane * 128;
-        bool small = false;
+        uint32_t small = 0;  // bit i: token 32 i + lane
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // units that spread over the banks, and over the columns
             const uint4 x = *reinterpret_cast<const uint4*>(at + i * 4096 + (((lane + (lane >> 3) + 4 * i) & 7) << 4));
-            small = small || (((x.x | x.y | x.z | x.w) & 0x40404040u) == 0 && 32 * i + lane < n);
+            if (((x.x | x.y | x.z | x.w) & 0x40404040u) == 0 && 32 * i + lane < n) small |= 1u << i;
         }
         const int hi = static_cast<int>(__reduce_max_sync(0xffffffffu, max(max(bits[0], bits[1]), max(bits[2], bits[3]))) >> 23);
         TileAsks ask = {half, 0u, before || hi + kFar <= run ? 1u : 0u, 0u};
         before = false;
-        if (__any_sync(0xffffffffu, small)) {
-            const uint2 l = look(tile, n, lane);
-            f = l.x;
-            ask.with_f = l.y & 1u;
+        if (__any_sync(0xffffffffu, small != 0)) {
+            const uint32_t l = look(tile, n, small, lane, fs);
+            ask.with_f = l & 1u;
             ask.eager |= ask.with_f;
             ask.half = ask.with_f ? -1.f : half;
-            before = l.y != 0;
+            before = l != 0;
         }
         run = ask.eager ? hi : max(run, hi);
         return ask;
     }
-    // Looks at the latent codes of all tokens, 16 a lane.  Returns f, and whether f are to be used (1), whether all
+    // Looks at all latent codes of the small tokens (the others count as 0).  Returns whether f are to be used (1), whether all
     // latents are small (2).
-    __device__ __noinline__ static uint2 look(const uint8_t* tile, int n, int lane) {
-        int f[4] = {0, 0, 0, 0}, g = kNoLatent;
-        const uint8_t* at = tile + (lane >> 3) * kBlock8Chunk + (lane & 7) * 16;
-#pragma unroll 4
-        for (int r = 0; r < n; ++r) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max_code16(*reinterpret_cast<const uint4*>(at + r * 128)));
-            const int e = top ? code_exp(top) : kNoLatent;
-            g = max(g, e);
+    __device__ __noinline__ static uint32_t look(const uint8_t* tile, int n, uint32_t small, int lane, int8_t* fs) {
+        int f[4], g = kNoLatent;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (4 * lane + k == r) f[k] = e;
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + lane;
+            f[i] = 0;
+            if (__any_sync(0xffffffffu, (small >> i & 1u) != 0)) {
+                const int e = latent_exp(tile + r * 128, r);
+                if (small >> i & 1u) f[i] = e;
+            }
+            if (r < n) g = max(g, f[i]);
         }
-        uint32_t packed = 0;
+        g = __reduce_max_sync(0xffffffffu, g);
         bool use = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            use = use || (4 * lane + i < n && (f[i] <= g - kFar || f[i] == kNoLatent));
-            f[i] = 4 * lane + i >= n ? 0 : f[i] == kNoLatent ? static_cast<int>(kZeroF) : max(f[i] - g, -7);
-            packed |= static_cast<uint32_t>(f[i] & 0xFF) << (8 * i);
+            use = use || (32 * i + lane < n && (f[i] <= g - kFar || f[i] == kNoLatent));
+            fs[32 * i + lane] = static_cast<int8_t>(f[i] == kNoLatent ? static_cast<int>(kZeroF) : max(f[i] - g, -7));
         }
         use = __any_sync(0xffffffffu, use);
-        return make_uint2(packed, (use ? 1u : 0u) | (g <= -kFar ? 2u : 0u));
+        __syncwarp();
+        return (use ? 1u : 0u) | (g <= -kFar ? 2u : 0u);
     }
 };
 

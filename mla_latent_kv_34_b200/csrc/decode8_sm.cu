@@ -7,11 +7,11 @@
 //                                           columns of their own, added at the end), or, where those do not fit, 32 of
 //                                           N = NR (lo as e5m2)
 // (NR: the rows rounded up to 16, 32 or 48).  Scores and O^T fit one SM's tensor memory, so a block is read once, by one
-// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token.  B 64, H 16, 4K: 41 us for the attend phase, 24 at a
-// copy's rate; once under way a tile takes 3600 cycles an SM (5.6 TB/s), the rest is the start (5500 cycles to the first
+// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token.  B 64, H 16, 4K: 44 us for the attend phase, 24 at a
+// copy's rate; once under way a tile takes 3800 cycles an SM (5.3 TB/s), the rest is the start (5500 cycles to the first
 // copy, then all SMs' first tiles at once) and the end (scores, softmax, aggregation and output of the last tile, 7000).
 // A ring of 2.75 tiles instead of two changed that by 2 %.  Waiting for the next tile's copies before the aggregation at hand
-// is issued, and a lo term with MMAs of its own, took 62 us.
+// is issued, and a lo term with MMAs of its own, took 62 us.  The form of 48 rows keeps 52 bytes a thread in local memory.
 //
 // Softmax: a thread per token (tensor-memory lane) and half the rows; a set of four warps has a tile's 128 tokens.  A row's
 // maximum over a warp's tokens is a warp reduction, then the set's warps exchange them at one barrier and each decides on
@@ -595,10 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                      mbar_wait(&bars[kBFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint32_t f;
-                const TileAsks ask = judge.judge(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf, f);
+                // (the buffer of f is free already: SEmpty of the tile before this one has been seen)
+                const TileAsks ask = judge.judge(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf,
+                                                 reinterpret_cast<int8_t*>(smem + L::kOffF) + (n & 3u) * kTile);
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[kBSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs));
-                if (ask.with_f) reinterpret_cast<uint32_t*>(smem + L::kOffF)[(n & 3u) * (kTile / 4) + lane] = f;
                 if (lane == 0) reinterpret_cast<TileAsks*>(smem + L::kOffAsk)[n & 3u] = ask;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[kBSFull + sb]);

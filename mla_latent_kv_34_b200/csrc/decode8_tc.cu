@@ -20,12 +20,16 @@
 // warp hands to the next as soon as its maximum is known; nothing else holds the warps in step.  P goes out in messages of
 // two units: staged in shared memory, one bulk copy to the O CTA's slot, whose barrier the O CTA arms itself.
 //
-// What bounds it: a tile takes about 3100 cycles; its score MMAs 2304, the S CTA's shared memory 2750 (MMA operands, copies
-// in and out, P, scales), a softmax warp's own instructions 2700.  At B 32, H 128, 8K the attend phase takes 86 to 92 us
-// (45 at the bf16 rate), of which 12 are the start (queries to codes, first tile) and as many a second sequence's start;
-// 4 x 128K 135 to 141 (89), ragged 128 x 2 tokens of 1 to 32K 1.0 ms (736 us), 1.2 ms under the power limit.  A first form
-// on CUDA cores took 7.3, 14.6 and 89 ms.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 ->
-// 93.9 us), all of a query's loads before the first is used (more registers and code: 91 -> 96 us).
+// What bounds it: a tile takes about 3200 cycles; its score MMAs 2304, the S CTA's shared memory 2850 (MMA operands, copies
+// in and out, P, scales), a softmax warp's own instructions 2800, in loops that fill the instruction cache: code that is seldom
+// run is kept short or called.  At B 32, H 128, 8K the attend phase takes 97 to 101 us (45 at the bf16 rate), of which 12 are the
+// start (queries to codes, first tile) and as many a second sequence's start; 4 x 128K 150 to 161 (89), ragged 128 x 2 tokens of
+// 1 to 32K 1.1 ms (736 us), 1.25 ms under the power limit.  A move of some row's reference costs the tile a pass over O, 1 us:
+// scores with a standard deviation of 3 at B 32, H 128, 8K take 207 us a call instead of 115.  A first form on CUDA cores took
+// 7.3, 14.6 and 89 ms; without the judging of tiles (TileAsks) and with a reference that only rises it took 86 to 92, 135 to
+// 141 us and 1.0 ms, and lost tails.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 -> 93.9 us),
+// all of a query's loads before the first is used (more registers and code: 91 -> 96 us), judging from global memory (its
+// requests share the path of shared memory: 108 -> 122 us a call).
 //
 // Every wait is bounded: on expiry the kernel records MLA_DEVERR_TIMEOUT, both CTAs of the pair abandon their loops,
 // let in-flight copies and MMAs land, free TMEM and return.
@@ -694,18 +698,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                          mbar_wait(&bars[kSBarFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    uint32_t f;
-                    const TileAsks ask =
-                        judge.judge(smem + kSOffRing + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf, f);
+                    // (the buffer of f is free already: SEmpty of the tile before this one has been seen)
+                    uint8_t* buf = smem + kSOffScale + (n % kScaleBufs) * kScaleBytes;
+                    const TileAsks ask = judge.judge(smem + kSOffRing + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane,
+                                                     Ref::kHalf, reinterpret_cast<int8_t*>(buf + kScaleF));
                     if (lane < 2) mbar_arrive(&bars[kSBarEmpty + 2 * sb + lane]);
                     ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
                     uint32_t e[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = __float_as_uint(static_cast<float>(static_cast<int>(bits[i] >> 23) - 127));
-                    uint8_t* to = smem + kSOffScale + (n % kScaleBufs) * kScaleBytes + 8 * lane;
+                    uint8_t* to = buf + 8 * lane;
                     const uint2 sc = make_uint2(__byte_perm(bits[0], bits[1], 0x7632), __byte_perm(bits[2], bits[3], 0x7632));
                     uint2 is = make_uint2(0x7F007F00u - sc.x, 0x7F007F00u - sc.y);
                     if (ask.with_f) {
+                        const uint32_t f = *reinterpret_cast<const uint32_t*>(buf + kScaleF + 4 * lane);
                         uint32_t up[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -717,7 +723,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         }
                         is.x += up[0] | (up[1] << 16);
                         is.y += up[2] | (up[3] << 16);
-                        *reinterpret_cast<uint32_t*>(to - 4 * lane + kScaleF) = f;
                     }
                     *reinterpret_cast<uint2*>(to) = sc;
                     *reinterpret_cast<uint2*>(to + 2 * kTile) =
