@@ -7,8 +7,8 @@
 //                                           columns of their own, added at the end), or, where those do not fit, 32 of
 //                                           N = NR (lo as e5m2)
 // (NR: the rows rounded up to 16, 32 or 48).  Scores and O^T fit one SM's tensor memory, so a block is read once, by one
-// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token.  B 64, H 16, 4K: 44 us for the attend phase, 24 at a
-// copy's rate; once under way a tile takes 3800 cycles an SM (5.3 TB/s), the rest is the start (5500 cycles to the first
+// SM, and nothing crosses SMs.  The bound is HBM: 580 bytes a token.  B 64, H 16, 4K: 45 us for the attend phase, 24 at a
+// copy's rate; once under way a tile takes 2.0 us an SM (5.5 TB/s), the rest is the start (5500 cycles to the first
 // copy, then all SMs' first tiles at once) and the end (scores, softmax, aggregation and output of the last tile, 7000).
 // A ring of 2.75 tiles instead of two changed that by 2 %.  Waiting for the next tile's copies before the aggregation at hand
 // is issued, and a lo term with MMAs of its own, took 62 us.  The form of 48 rows keeps 52 bytes a thread in local memory.

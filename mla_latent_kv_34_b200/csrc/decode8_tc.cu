@@ -20,14 +20,15 @@
 // warp hands to the next as soon as its maximum is known; nothing else holds the warps in step.  P goes out in messages of
 // two units: staged in shared memory, one bulk copy to the O CTA's slot, whose barrier the O CTA arms itself.
 //
-// What bounds it: a tile takes about 3200 cycles; its score MMAs 2304, the S CTA's shared memory 2850 (MMA operands, copies
-// in and out, P, scales), a softmax warp's own instructions 2800, in loops that fill the instruction cache: code that is seldom
-// run is kept short or called.  At B 32, H 128, 8K the attend phase takes 97 to 101 us (45 at the bf16 rate), of which 12 are the
-// start (queries to codes, first tile) and as many a second sequence's start; 4 x 128K 150 to 161 (89), ragged 128 x 2 tokens of
-// 1 to 32K 1.1 ms (736 us), 1.25 ms under the power limit.  A move of some row's reference costs the tile a pass over O, 1 us:
+// What bounds it: a tile takes 2.2 us (4 sequences over 8 to 40 tiles a pair), for 2304 cycles of score MMAs, 2880 of the S CTA's
+// shared memory (MMA operands, copies in and out, P, scales) and 2800 of a softmax warp's instructions, in loops that fill the
+// instruction cache: code that is seldom run is kept short or called.  At B 32, H 128, 8K the attend phase takes 97 to 101 us
+// (45 at the bf16 rate), of which 12 are the
+// start (queries to codes, first tile) and as many a second sequence's start; 4 x 128K 161 (89), ragged 128 x 2 tokens of
+// 1 to 32K 1.29 ms a call (736 us).  A move of some row's reference costs the tile a pass over O, 1 us:
 // scores with a standard deviation of 3 at B 32, H 128, 8K take 207 us a call instead of 115.  A first form on CUDA cores took
-// 7.3, 14.6 and 89 ms; without the judging of tiles (TileAsks) and with a reference that only rises it took 86 to 92, 135 to
-// 141 us and 1.0 ms, and lost tails.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 -> 93.9 us),
+// 7.3, 14.6 and 89 ms; without the judging of tiles (TileAsks) and with a reference that only rises it took 1.95 to 2.05 us a
+// tile, 1.18 ms a ragged call, and lost tails.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 -> 93.9 us),
 // all of a query's loads before the first is used (more registers and code: 91 -> 96 us), judging from global memory (its
 // requests share the path of shared memory: 108 -> 122 us a call).
 //
