@@ -280,16 +280,16 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
  * rounding of either (query elements below 2^-9 of their row's largest are
  * held to 2^-17 of it); their sums, the softmax and its sums are fp32.  In the
  * aggregation a token's weight p_t s_t has 8 significant bits, as mla_decode's
- * probabilities have, down to about 2^-12 of the largest of its row; smaller
- * ones are rounded to steps of 2^-21 of it (2^-18 for n_q * H <= 32) so that
- * their sum is kept, and follow the row where it falls: the largest is judged
- * by tiles of 128 tokens as they come, and by the tokens' latent values, so
- * that a scale set by k^R, or the scale 1 of a row of zeros, costs the others
- * nothing.  Beside a token whose k^R is 2^4 to 2^8 times its latent values the
- * others of its 32 (128) have up to that much less.  What lies 2^-48 below the
- * largest is lost.  A NaN among a row's visible tokens, or a NaN or infinity in
- * its query, makes its out and lse NaN; one in a later token of the step, which
- * the row does not see, does not reach it.
+ * probabilities have, down to 2^-7 of the largest of its row at the least;
+ * smaller ones are rounded, to steps of 2^-16 of it at the most, in a way that
+ * keeps their sum, and more exactly where the row falls for good: the largest
+ * is taken by tiles of 128 tokens as they come, and by the tokens' latent
+ * values, so that a scale set by k^R, or the scale 1 of a row of zeros, costs
+ * the others nothing.  Beside a token whose k^R is 2^4 to 2^8 times its latent
+ * values the others of its 32 (128) have up to that much less.  What lies 2^-48
+ * below the largest is lost.  A NaN among a row's visible tokens, or a NaN or
+ * infinity in its query, makes its out and lse NaN; one in a later token of the
+ * step, which the row does not see, does not reach it.
  */
 size_t mla_decode8_workspace_bytes(int B, int n_q, int H, int num_splits);
 mla_status mla_decode8(const void* q, const void* cache8, int64_t cap_blocks,

@@ -325,20 +325,20 @@ static __device__ __noinline__ void nan_to_zero_row(uint8_t* row) {
     for (int u = 0; u < 32; ++u) nan_to_zero16(row + (u >> 3) * kBlock8Chunk + (u & 7) * 16);
 }
 
-// One warp judges the tiles of a segment one after another, from the codes that the copies brought to shared memory.  (The
+// One warp scans the tiles of a segment one after another, from the codes that the copies brought to shared memory.  (The
 // code of the common case is kept short: the loops of a block's warps share an instruction cache that they fill.)
-struct TileJudge {
+struct TileScan {
     int run;      // largest scale since the last eager tile
     bool before;  // the tile before may have set R by its scales
     __device__ __forceinline__ void reset() {
         run = -1000;
         before = false;
     }
-    // The tile's codes are at `tile`, its first n >= 1 tokens exist; `bits`: the scales of tokens 4 lane .. 4 lane + 3 (kNoScale for
+    // A tile's codes are at `codes`, its first n >= 1 tokens exist; `bits`: the scales of tokens 4 lane .. 4 lane + 3 (kNoScale for
     // those that do not).  Where f are in use, the tokens' go to `fs` (int8, in shared memory).
-    __device__ __forceinline__ TileAsks judge(const uint8_t* tile, int n, const uint32_t (&bits)[4], int lane, float half, int8_t* fs) {
+    __device__ __forceinline__ TileAsks tile(const uint8_t* codes, int n, const uint32_t (&bits)[4], int lane, float half, int8_t* fs) {
         // 16 codes of a token, none of which is 2 = 448 * 2^-7.8 or more: the upper exponent bit is not set
-        const uint8_t* at = tile + lane * 128;
+        const uint8_t* at = codes + lane * 128;
         uint32_t small = 0;  // bit i: token 32 i + lane
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // units that spread over the banks, and over the columns
@@ -349,7 +349,7 @@ struct TileJudge {
         TileAsks ask = {half, 0u, before || hi + kFar <= run ? 1u : 0u, 0u};
         before = false;
         if (__any_sync(0xffffffffu, small != 0)) {
-            const uint32_t l = look(tile, n, small, lane, fs);
+            const uint32_t l = look(codes, n, small, lane, fs);
             ask.with_f = l & 1u;
             ask.eager |= ask.with_f;
             ask.half = ask.with_f ? -1.f : half;
@@ -360,14 +360,14 @@ struct TileJudge {
     }
     // Looks at all latent codes of the small tokens (the others count as 0).  Returns whether f are to be used (1), whether all
     // latents are small (2).
-    __device__ __noinline__ static uint32_t look(const uint8_t* tile, int n, uint32_t small, int lane, int8_t* fs) {
+    __device__ __noinline__ static uint32_t look(const uint8_t* codes, int n, uint32_t small, int lane, int8_t* fs) {
         int f[4], g = kNoLatent;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = 32 * i + lane;
             f[i] = 0;
             if (__any_sync(0xffffffffu, (small >> i & 1u) != 0)) {
-                const int e = latent_exp(tile + r * 128, r);
+                const int e = latent_exp(codes + r * 128, r);
                 if (small >> i & 1u) f[i] = e;
             }
             if (r < n) g = max(g, f[i]);

@@ -31,7 +31,7 @@ using namespace d8;
 
 constexpr int kChunk = kBlock8Chunk;
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
-constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpJudge = 10, kWarpEpi = 12;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpScan = 10, kWarpEpi = 12;
 constexpr int kThreads = 512;
 
 constexpr uint32_t kNbSet = 1;  // named barriers 1, 2: the four softmax warps of a set
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             mbar_init(&bars[kBEmpty + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[kBSFull + i], 2);  // the scores' MMAs and the judge
+            mbar_init(&bars[kBSFull + i], 2);  // the scores' MMAs and the scan of its rows
             mbar_init(&bars[kBSEmpty + i], kSoftThreads);
             mbar_init(&bars[kBPReady + i], kSoftThreads);
             mbar_init(&bars[kBPFree + i], 1);
@@ -560,14 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             ++kseg;
         }
         if (!ok) raise_abort(abort_flag, p.dev_status);
-    } else if (warp == kWarpJudge) {
+    } else if (warp == kWarpScan) {
         // ---- what each tile asks of the references (TileAsks), ahead of the softmax, which is past tile n - 3 where it has read
         //      the scores of tile n - 2.  A tile's codes stay until its aggregation, after the softmax.
         SegWalk w = walk;
         Seg s;
         uint32_t n = 0;
         bool ok = true;
-        TileJudge judge;
+        TileScan scan;
         uint32_t next[4];
         while (ok && w.next(p, s)) {
             auto entry = [&](int t) { return t < s.t1 ? s.tab[t] : 0; };
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             // the scales are asked for a tile ahead, the table entry two
             load(s.t0, entry(s.t0));
             int32_t e1 = entry(s.t0 + 1);
-            judge.reset();
+            scan.reset();
             for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                 uint32_t bits[4];
 #pragma unroll
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 // (the buffer of f is free already: SEmpty of the tile before this one has been seen)
-                const TileAsks ask = judge.judge(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf,
+                const TileAsks ask = scan.tile(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf,
                                                  reinterpret_cast<int8_t*>(smem + L::kOffF) + (n & 3u) * kTile);
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[kBSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs));
                 if (lane == 0) reinterpret_cast<TileAsks*>(smem + L::kOffAsk)[n & 3u] = ask;

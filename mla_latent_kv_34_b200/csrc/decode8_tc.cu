@@ -27,9 +27,9 @@
 // start (queries to codes, first tile) and as many a second sequence's start; 4 x 128K 161 (89), ragged 128 x 2 tokens of
 // 1 to 32K 1.29 ms a call (736 us).  A move of some row's reference costs the tile a pass over O, 1 us:
 // scores with a standard deviation of 3 at B 32, H 128, 8K take 207 us a call instead of 115.  A first form on CUDA cores took
-// 7.3, 14.6 and 89 ms; without the judging of tiles (TileAsks) and with a reference that only rises it took 1.95 to 2.05 us a
+// 7.3, 14.6 and 89 ms; without the scan of the tiles (TileAsks) and with a reference that only rises it took 1.95 to 2.05 us a
 // tile, 1.18 ms a ragged call, and lost tails.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 -> 93.9 us),
-// all of a query's loads before the first is used (more registers and code: 91 -> 96 us), judging from global memory (its
+// all of a query's loads before the first is used (more registers and code: 91 -> 96 us), scanning from global memory (its
 // requests share the path of shared memory: 108 -> 122 us a call).
 //
 // Every wait is bounded: on expiry the kernel records MLA_DEVERR_TIMEOUT, both CTAs of the pair abandon their loops,
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
         if (rank == 0) {
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&bars[kSBarFull + i], 1);
-                mbar_init(&bars[kSBarEmpty + i], 2);  // the scores' MMAs and the judge
+                mbar_init(&bars[kSBarEmpty + i], 2);  // the scores' MMAs and the scan of its rows
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bars[kSBarSFull + i], 2);  // the scores' MMAs and the scales
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             Seg s;
             uint32_t n = 0;
             bool ok = true;
-            TileJudge judge;
+            TileScan scan;
             uint32_t next[4];
             while (ok && w.next(p, s)) {
                 auto entry = [&](int t) { return t < s.t1 ? s.tab[t] : 0; };
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 // the scales are asked for a tile ahead, the table entry two
                 load(s.t0, entry(s.t0));
                 int32_t e1 = entry(s.t0 + 1);
-                judge.reset();
+                scan.reset();
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                     uint32_t bits[4];
 #pragma unroll
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     if (!ok) break;
                     // (the buffer of f is free already: SEmpty of the tile before this one has been seen)
                     uint8_t* buf = smem + kSOffScale + (n % kScaleBufs) * kScaleBytes;
-                    const TileAsks ask = judge.judge(smem + kSOffRing + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane,
+                    const TileAsks ask = scan.tile(smem + kSOffRing + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane,
                                                      Ref::kHalf, reinterpret_cast<int8_t*>(buf + kScaleF));
                     if (lane < 2) mbar_arrive(&bars[kSBarEmpty + 2 * sb + lane]);
                     ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);

@@ -237,3 +237,31 @@ def test_decode8_rows_at_the_smallest_scale(H, a):
     """Rows whose scale is 2^-40, the least there is, and queries as large; W^UV brings the output back to the order of 1."""
     p = Problem8([300, 70], H, 1, rows=lambda b, x: bf16_values(small_rows(len(x), a, seed=b)), q=lambda v: 0.5 * v / a)
     check(scaled_up(p, -round(np.log2(a))), num_splits=1)
+
+
+@pytest.mark.parametrize("H,n_q,splits", [(16, 1, 0), (16, 1, 5), (24, 2, 3), (40, 1, 4), (128, 1, 0), (128, 2, 6), (20, 40, 2)])
+def test_decode8_ragged_peaks_zeros_and_scales_together(H, n_q, splits):
+    """Sequences of every kind behind one another in a work unit (each with its own peaks and scales), ten times bit for bit."""
+    lengths = [700, 41, 1300, 128, 257, 90, 3000, 45, 640, 2100]
+
+    def rows(b, x):
+        n = len(x)
+        y = peaked_rows(n, 0.3, at=(17 * b) % n, ratio=(1.0, 300.0, 8.0)[b % 3], seed=b)
+        if b % 2:
+            y[(5 + b) % n::61] = 0.0
+        if b % 4 == 1:
+            y *= 2.0 ** -15
+        return bf16_values(y)
+
+    def q(v):
+        v = peaked_queries(v.shape[:-1])
+        for b in range(len(lengths)):
+            if b % 4 == 1:
+                v[b * n_q:(b + 1) * n_q] *= 2.0 ** 15
+        return v
+    p = Problem8(lengths, H, n_q, rows=rows, q=q)
+    check(p, num_splits=splits)
+    out, lse = p.decode(num_splits=splits)
+    for _ in range(10):
+        o2, l2 = p.decode(num_splits=splits)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
