@@ -285,9 +285,9 @@ mla_status mla_read_cache8(const void* cache8, int64_t cap_blocks8, const int32_
  * keeps their sum, and more exactly where the row falls for good: the largest
  * is taken by tiles of 128 tokens as they come, and by the tokens' latent
  * values, so that a scale set by k^R, or the scale 1 of a row of zeros, costs
- * the others nothing.  Beside a token whose k^R is 2^4 to 2^8 times its latent
- * values the others of its 32 (128) have up to that much less.  What lies 2^-48
- * below the largest is lost.  A NaN among a row's visible tokens, or a NaN or
+ * the others nothing (a k^R up to 2^4 times the token's latent values costs the
+ * others of its 32 or 128 up to that much).  What lies 2^-48 below the largest
+ * is lost.  A NaN among a row's visible tokens, or a NaN or
  * infinity in its query, makes its out and lse NaN; one in a later token of the
  * step, which the row does not see, does not reach it.
  */

@@ -255,23 +255,20 @@ struct LowUnit {  // a warp's last low unit of a row: its largest y, its tile (c
     float top;
     uint32_t at;
 };
-// What a tile's rows ask of R.  A row's scale covers its RoPE columns, and is 1 for a row of zeros, so a token may have a large
-// y and add little or nothing to O, while the others in its unit are held in steps set by it.  So one warp looks at the
-// rows ahead of the softmax: at 16 of each token's latent codes, and at all of them where those are below 448 * 2^-7.8.
-//   f     the exponent of a token's largest latent code against 448, less the largest such in the tile, added to its y where
-//         R is chosen.  -7 at least: with R + 1.75 instead of R + 8.75 as the limit of y + f (`room`), its P' stays below 448.
-//         Used where some f is -4 or less, or some token's latents are all zero: such a token has no P' to hold, so its y is
-//         taken kZeroDown lower everywhere (so that its P' is small and sets nothing) but in the sums; its f is kZeroF.
-//   eager what set R may have been large by its scale alone: f are in use, or were in the tile before, or its latents were all
-//         small against their scales, or the scales have fallen by 2^4 since this last was so.  Low units move R at once.
+// A row's scale covers its RoPE columns, and is 1 for a row of zeros, so a token may have a large y and add little or nothing to
+// O, while the others in its unit are held in steps set by it.  So one warp looks at the rows ahead of the softmax: at 16 of
+// each token's latent codes, and at all of them where those are below 448 * 2^-3.8.
+//   lift   m, for tokens whose latent codes are small beside the largest in the tile: the power of two by which they may be
+//          multiplied, up to 2^15.  In the aggregation such a token's codes are multiplied by 2^m (exactly; in shared memory) and its
+//          scale divided by it.  A token whose latents are all zero has m = kZeroLift, and no codes to multiply.
+//   eager  what set R may have been large by its scale alone: tokens are lifted, or were in the tile before, or its latents were
+//          all small against their scales, or the scales have fallen by 2^4 since this last was so.  Low units move R at once.
 // 511 rows of standard deviation a and one of zeros in their midst lost 0.06 of the result at a = 0.01, all of it at 1e-5.
-constexpr float kRoom = 8.75f, kRoomF = 1.75f;
+constexpr float kRoom = 8.75f;
 constexpr int kFar = 4;
-constexpr float kZeroF = 1.f, kZeroDown = 40.f;
+constexpr int kMostLift = 15, kZeroLift = 40;
 struct TileAsks {
-    float half;  // RowRef::stays: negative where f are in use
-    uint32_t with_f, eager, pad;
-    __device__ __forceinline__ float room() const { return with_f ? kRoomF : kRoom; }
+    uint32_t lift, eager;
 };
 constexpr int kNoLatent = -99;
 constexpr uint32_t kNoScale = 0x0D800000u;  // 2^-100, for tokens that do not exist (their scores are masked)
@@ -325,6 +322,70 @@ static __device__ __noinline__ void nan_to_zero_row(uint8_t* row) {
     for (int u = 0; u < 32; ++u) nan_to_zero16(row + (u >> 3) * kBlock8Chunk + (u & 7) * 16);
 }
 
+// 16 codes times 2^m, in place (no result passes 448).
+__device__ __forceinline__ void lift16(uint8_t* at, uint32_t pow2_f16x2) {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2];
+        uint16_t c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[k]) : "r"(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> (16 * k)))), "r"(pow2_f16x2));
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c[k]) : "r"(h[k]));
+        }
+        w[i] = c[0] | static_cast<uint32_t>(c[1]) << 16;
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// A token's row of latent codes times 2^m, by a thread.
+static __device__ __noinline__ void lift_row(uint8_t* row, int m) {
+    if (m < 1 || m > kMostLift) return;
+    const uint32_t p = static_cast<uint32_t>(15 + m) << 10;
+#pragma unroll 1
+    for (int u = 0; u < 32; ++u) lift16(row + (u >> 3) * kBlock8Chunk + (u & 7) * 16, p | p << 16);
+}
+
+// Bit i: of 16 codes of token 32 i + lane none is 2^5 = 448 * 2^-3.8 or more (the upper two exponent bits are not both set).
+__device__ __forceinline__ uint32_t small_tokens(const uint8_t* codes, int n, int lane) {
+    const uint8_t* at = codes + lane * 128;
+    uint32_t small = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // units that spread over the banks, and over the columns
+        const uint4 x = *reinterpret_cast<const uint4*>(at + i * 4096 + (((lane + (lane >> 3) + 4 * i) & 7) << 4));
+        const uint32_t m = (x.x & (x.x << 1)) | (x.y & (x.y << 1)) | (x.z & (x.z << 1)) | (x.w & (x.w << 1));
+        if ((m & 0x40404040u) == 0 && 32 * i + lane < n) small |= 1u << i;
+    }
+    return small;
+}
+// The lifts of tokens 32 i + lane of a tile (byte i of the first; 0 for those not in `small`); the second: whether any is lifted (1),
+// whether all latents are small (2).
+static __device__ __noinline__ uint2 tile_lifts(const uint8_t* codes, int n, uint32_t small, int lane) {
+    int f[4], g = kNoLatent;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 32 * i + lane;
+        f[i] = 0;
+        if (__any_sync(0xffffffffu, (small >> i & 1u) != 0)) {
+            const int e = latent_exp(codes + r * 128, r);
+            if (small >> i & 1u) f[i] = e;
+        }
+        if (r < n) g = max(g, f[i]);
+    }
+    g = __reduce_max_sync(0xffffffffu, g);
+    uint32_t lifts = 0;
+    bool use = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = f[i] == kNoLatent ? kZeroLift : min(g - f[i], kMostLift);
+        use = use || ((small >> i & 1u) != 0 && m >= kFar);
+        if (small >> i & 1u) lifts |= static_cast<uint32_t>(max(m, 0)) << (8 * i);
+    }
+    use = __any_sync(0xffffffffu, use);
+    return make_uint2(use ? lifts : 0u, (use ? 1u : 0u) | (g <= -kFar ? 2u : 0u));
+}
+
 // One warp scans the tiles of a segment one after another, from the codes that the copies brought to shared memory.  (The
 // code of the common case is kept short: the loops of a block's warps share an instruction cache that they fill.)
 struct TileScan {
@@ -335,53 +396,23 @@ struct TileScan {
         before = false;
     }
     // A tile's codes are at `codes`, its first n >= 1 tokens exist; `bits`: the scales of tokens 4 lane .. 4 lane + 3 (kNoScale for
-    // those that do not).  Where f are in use, the tokens' go to `fs` (int8, in shared memory).
-    __device__ __forceinline__ TileAsks tile(const uint8_t* codes, int n, const uint32_t (&bits)[4], int lane, float half, int8_t* fs) {
-        // 16 codes of a token, none of which is 2 = 448 * 2^-7.8 or more: the upper exponent bit is not set
-        const uint8_t* at = codes + lane * 128;
-        uint32_t small = 0;  // bit i: token 32 i + lane
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // units that spread over the banks, and over the columns
-            const uint4 x = *reinterpret_cast<const uint4*>(at + i * 4096 + (((lane + (lane >> 3) + 4 * i) & 7) << 4));
-            if (((x.x | x.y | x.z | x.w) & 0x40404040u) == 0 && 32 * i + lane < n) small |= 1u << i;
-        }
+    // those that do not).  Where tokens are lifted, the tile's lifts go to `to` (a byte each, in shared memory).
+    __device__ __forceinline__ TileAsks tile(const uint8_t* codes, int n, const uint32_t (&bits)[4], int lane, uint8_t* to) {
+        const uint32_t small = small_tokens(codes, n, lane);
         const int hi = static_cast<int>(__reduce_max_sync(0xffffffffu, max(max(bits[0], bits[1]), max(bits[2], bits[3]))) >> 23);
-        TileAsks ask = {half, 0u, before || hi + kFar <= run ? 1u : 0u, 0u};
+        TileAsks ask = {0u, before || hi + kFar <= run ? 1u : 0u};
         before = false;
         if (__any_sync(0xffffffffu, small != 0)) {
-            const uint32_t l = look(codes, n, small, lane, fs);
-            ask.with_f = l & 1u;
-            ask.eager |= ask.with_f;
-            ask.half = ask.with_f ? -1.f : half;
-            before = l != 0;
+            const uint2 l = tile_lifts(codes, n, small, lane);
+            ask.lift = l.y & 1u;
+            ask.eager |= ask.lift;
+            before = l.y != 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[32 * i + lane] = static_cast<uint8_t>(l.x >> (8 * i));
+            __syncwarp();
         }
         run = ask.eager ? hi : max(run, hi);
         return ask;
-    }
-    // Looks at all latent codes of the small tokens (the others count as 0).  Returns whether f are to be used (1), whether all
-    // latents are small (2).
-    __device__ __noinline__ static uint32_t look(const uint8_t* codes, int n, uint32_t small, int lane, int8_t* fs) {
-        int f[4], g = kNoLatent;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 32 * i + lane;
-            f[i] = 0;
-            if (__any_sync(0xffffffffu, (small >> i & 1u) != 0)) {
-                const int e = latent_exp(codes + r * 128, r);
-                if (small >> i & 1u) f[i] = e;
-            }
-            if (r < n) g = max(g, f[i]);
-        }
-        g = __reduce_max_sync(0xffffffffu, g);
-        bool use = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            use = use || (32 * i + lane < n && (f[i] <= g - kFar || f[i] == kNoLatent));
-            fs[32 * i + lane] = static_cast<int8_t>(f[i] == kNoLatent ? static_cast<int>(kZeroF) : max(f[i] - g, -7));
-        }
-        use = __any_sync(0xffffffffu, use);
-        __syncwarp();
-        return (use ? 1u : 0u) | (g <= -kFar ? 2u : 0u);
     }
 };
 
@@ -391,10 +422,10 @@ struct RowPeak {  // of a row's piece: the y (rounded up) that the last first, u
 };
 template <int First, int Up, int Low>
 struct RowRef {
-    // The common case, in one comparison: neither up nor low (nor f in use).
+    // The common case, in one comparison: neither up nor low.
     static constexpr float kMiddle = 0.5f * (kRoom - Low), kHalf = 0.5f * (kRoom + Low);
-    __device__ static bool stays(float top, float R, float half) { return !(fabsf(top - R - kMiddle) > half); }
-    __device__ static bool is_up(float top, float R, float room) { return top > R + room; }
+    __device__ static bool stays(float top, float R) { return !(fabsf(top - R - kMiddle) > kHalf); }
+    __device__ static bool is_up(float top, float R) { return top > R + kRoom; }
     // (not for a unit with nothing visible, nor before the first)
     __device__ static bool is_low(float top, float R) {
         return top < R - static_cast<float>(Low) && top != __uint_as_float(kMinusInf);
@@ -406,23 +437,21 @@ struct RowRef {
         pk.peak = ceilf(top);
         return pk.high = pk.peak - First;
     }
-    // The reference after a unit of tile n whose largest y + f is `top`; `same`: R has not changed since this warp's last
-    // unit, of tile n - 1.  `low` is the warp's for the row.
-    __device__ static float moved(float top, float R, bool same, uint32_t n, TileAsks ask, LowUnit& low, RowPeak& pk) {
-        const bool with_f = ask.with_f;
-        const int first_at = with_f ? 1 : First;
-        if (is_up(top, R, ask.room())) {
+    // The reference after a unit of tile n whose largest y is `top`; `same`: R has not changed since this warp's last unit, of
+    // tile n - 1.  `low` is the warp's for the row.
+    __device__ static float moved(float top, float R, bool same, uint32_t n, bool eager, LowUnit& low, RowPeak& pk) {
+        if (is_up(top, R)) {
             const bool first = R == kNoRef;
             pk.peak = ceilf(top);
-            R = pk.peak - (first || with_f ? first_at : Up);
+            R = pk.peak - (first ? First : Up);
             pk.high = first ? R : fmaxf(pk.high, R);
         } else if (is_low(top, R)) {
-            if (ask.eager) {
+            if (eager) {
                 pk.peak = ceilf(top);
-                R = fminf(R, fmaxf(pk.peak - first_at, pk.high - kLift));
+                R = fminf(R, fmaxf(pk.peak - First, pk.high - kLift));
                 low.at = kNoTile;
             } else if (same && low.at == n - 1) {
-                R = fminf(R, fmaxf(ceilf(fmaxf(top, low.top)) - first_at, pk.peak - Up));
+                R = fminf(R, fmaxf(ceilf(fmaxf(top, low.top)) - First, pk.peak - Up));
                 low.at = kNoTile;
             } else {
                 low.top = top;

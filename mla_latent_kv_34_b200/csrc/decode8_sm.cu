@@ -58,9 +58,9 @@ struct Lay {
     static constexpr int kOffL = kOffRef + 8 * kRN * 4;      // [8 warps][kRN] a segment's sums
     static constexpr int kOffT = kOffL + 8 * kRN * 4;        // [8 warps][kRN] the second sums (not kStack)
     static constexpr int kOffLR = kOffT + (kStack ? 0 : 8 * kRN * 4);  // [2 sets][kRN] its references
-    static constexpr int kOffF = kOffLR + 2 * kRN * 4;       // [4 tiles][128] f of the tokens (int8)
+    static constexpr int kOffF = kOffLR + 2 * kRN * 4;       // [4 tiles][128] lifts of the tokens
     static constexpr int kOffAsk = kOffF + 4 * kTile;        // [4 tiles] TileAsks
-    static constexpr int kOffBar = kOffAsk + 4 * 16;
+    static constexpr int kOffBar = kOffAsk + 4 * 8;
     static constexpr int kOffTail = kOffBar + kNumBars * 8;  // tmem base, abort flag, rescale place, [total, sequence, tile]
     static constexpr int kSmemBytes = kOffTail + 32;
     static_assert(2 * kN + 4 * kOC <= 512, "tensor memory");
@@ -401,8 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
             const int lim0 = s.L - p.n_q + 1;  // keys below this are visible to every query of the step
             for (int t = s.t0; t < s.t1; ++t, ++n) {
                 const uint32_t sb = n & 1u, us = n >> 1;
-                const float st = __uint_as_float(sc), inv_s = __uint_as_float(0x7F000000u - sc);
-                const float et = static_cast<float>(static_cast<int>(sc >> 23) - 127);
+                const float st = __uint_as_float(sc);
+                float inv_s = __uint_as_float(0x7F000000u - sc);
+                float et = static_cast<float>(static_cast<int>(sc >> 23) - 127);
                 sc = scale_bits(e1, t + 1);
                 e1 = entry(t + 2);
                 ok = mbar_wait(&bars[kBSFull + sb], us & 1u, abort_flag, kLimitNs) && ok;
@@ -423,6 +424,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 tc_fence_before();
                 mbar_arrive(&bars[kBSEmpty + sb]);
                 const int tok = t * kTile + tk;
+                const TileAsks& ask = reinterpret_cast<const TileAsks*>(smem + L::kOffAsk)[n & 3u];
+                if (ask.lift) {
+                    const int m = smem[L::kOffF + (n & 3u) * kTile + tk];
+                    if (m > 0 && tok < s.L) {
+                        et -= static_cast<float>(m);
+                        inv_s *= exp2_int(m);
+                        if (set == 0) {  // (the scores are formed)
+                            ok = mbar_wait(&bars[kBFull + 2 * sb], us & 1u, abort_flag, kLimitNs) &&
+                                 mbar_wait(&bars[kBFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs) && ok;
+                            lift_row(smem + L::kOffRing + sb * kTileBytes + tk * 128, m);
+                        }
+                    }
+                    __syncwarp();
+                }
                 // y = log2(p s_t), before the reference
 #pragma unroll
                 for (int i = 0; i < RN; ++i) y[i] = fmaf(y[i] * st, rowf[i], et);
@@ -439,23 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     for (int i = 0; i < RN; ++i)
                         if (tok >= lim0 + (row0 + i) / p.H) y[i] = -CUDART_INF_F;
                 }
-                const TileAsks& ask = reinterpret_cast<const TileAsks*>(smem + L::kOffAsk)[n & 3u];
                 // the tile's row maxima: lane i gets row row0 + i's over the warp's tokens, then over the set's
                 float top = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < RN; ++i) {
                     const float v = warp_max_f32(y[i]);
                     if (lane == i) top = v;
-                }
-                float f = 0.f;
-                if (ask.with_f) {
-                    f = static_cast<float>(reinterpret_cast<const int8_t*>(smem + L::kOffF)[(n & 3u) * kTile + tk]);
-#pragma unroll
-                    for (int i = 0; i < RN; ++i) {
-                        if (f == kZeroF) y[i] -= kZeroDown;
-                        const float v = warp_max_f32(y[i] + f);
-                        if (lane == i) top = v;
-                    }
                 }
                 float* mx = reinterpret_cast<float*>(smem + L::kOffMax) + (8 * sb + 4 * set) * RN;
                 if (lane < RN) mx[qd * RN + lane] = top;
@@ -469,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                 const uint32_t dither = dither0 + dither_mask(tk >> 4, t);
                 if (t == s.t0 && R == kNoRef) R = Ref::first(top, peak);
                 int d = 0;
-                if (!__all_sync(0xffffffffu, Ref::stays(top, R, ask.half))) {
+                if (!__all_sync(0xffffffffu, Ref::stays(top, R))) {
                     const float was = R;
-                    R = Ref::moved(top, R, t > s.t0, n, ask, low, peak);
+                    R = Ref::moved(top, R, t > s.t0, n, ask.eager != 0, low, peak);
                     d = ref_exp(was, R);
                 }
                 if (__any_sync(0xffffffffu, d != 0)) {
@@ -483,16 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                     }
                 }
                 if (lane < RN) refs[lane] = R;
-                __syncwarp();
-                if (f == kZeroF) {
-                    // a token whose latents are all zero: what the sums lack
-#pragma unroll
-                    for (int i = 0; i < RN; ++i) {
-                        const float a = ex2_approx(y[i] + kZeroDown - refs[i]) * inv_s;
-                        lp[i] += a;
-                        if (!L::kStack) tp[i] += a;
-                    }
-                }
                 __syncwarp();
                 uint32_t hi[RN / 4], lo[RN / 4];
 #pragma unroll
@@ -595,9 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_sm_kernel(const Params p)
                      mbar_wait(&bars[kBFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                // (the buffer of f is free already: SEmpty of the tile before this one has been seen)
-                const TileAsks ask = scan.tile(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane, Ref::kHalf,
-                                                 reinterpret_cast<int8_t*>(smem + L::kOffF) + (n & 3u) * kTile);
+                // (the buffer of lifts is free already: SEmpty of the tile before this one has been seen)
+                const TileAsks ask = scan.tile(smem + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane,
+                                                smem + L::kOffF + (n & 3u) * kTile);
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[kBSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs));
                 if (lane == 0) reinterpret_cast<TileAsks*>(smem + L::kOffAsk)[n & 3u] = ask;
                 __syncwarp();

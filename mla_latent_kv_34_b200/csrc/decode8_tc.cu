@@ -50,7 +50,7 @@ constexpr int kVBytes = 4 * kChunk;               // O CTA: a V stage = the four
 constexpr int kVStages = 2;
 constexpr int kUnit = kTile / 4;                  // tokens of a unit: a quarter tile
 constexpr int kPBytes = kRows * 128;              // a P message: two units, [128 rows x (hi 64 tokens | lo 64 tokens)]
-constexpr int kMsgBytes = kPBytes + 2 * kRows;    // P | per unit and row the rescale exponent (int8): one bulk copy
+constexpr int kMsgBytes = kPBytes + 2 * kRows + 16;  // P | per unit and row the rescale exponent (int8) | the tile is lifted
 constexpr int kMsgStride = 17408;                 // 1024-aligned
 constexpr int kPSlots = 5;                        // O CTA: message slots
 constexpr int kStages = 3;                        // S CTA: staging buffers
@@ -70,7 +70,7 @@ constexpr int kSOffQR = 2 * kTileBytes;                // RoPE part of Q: [128 r
 constexpr int kSOffStage = kSOffQR + kRows * 128;      // kStages staging buffers, kMsgStride apart
 constexpr int kScaleBufs = 4;
 constexpr int kScaleInv = 2 * kTile * 2, kScaleF = 3 * kTile * 2, kScaleFlags = kScaleF + kTile;  // within a buffer
-constexpr int kScaleBytes = kScaleFlags + 16;          // a tile's token scales s, log2 s and 1 / s as bf16 (all exact), f as int8; TileAsks
+constexpr int kScaleBytes = kScaleFlags + 16;          // a tile's token scales s, log2 s and 1 / s as bf16 (all exact), lifts; TileAsks
 constexpr int kSOffScale = kSOffStage + kStages * kMsgStride;
 constexpr int kSOffRef = kSOffScale + kScaleBufs * kScaleBytes;  // [4][128] reference exponents handed on
 constexpr int kSOffLx = kSOffRef + 4 * kRows * 4;      // [3][3][128] a segment's two sums and R of the first three quarters
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         RA = ref_in[lane & 15];
                         RB = ref_in[16 + (lane & 15)];
                     }
-                    float top = lane < 16 ? mA : mB;
+                    const float top = lane < 16 ? mA : mB;
                     float last = R;  // this warp's last unit's: the sums are relative to it
                     R = lane < 16 ? RA : RB;
                     if (t == s.t0) {  // (nothing in the sums yet)
@@ -535,23 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         }
                         last = R;
                     }
-                    if (!__all_sync(0xffffffffu, Ref::stays(top, R, ask->half))) {
-                        if (ask->with_f) {
-                            mA = mB = -CUDART_INF_F;
-                            const uint4 fw = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(sw4) - 2 * cb + kScaleF + cb);
-                            const uint32_t f4[4] = {fw.x, fw.y, fw.z, fw.w};
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float f = static_cast<float>(static_cast<int8_t>(f4[i / 4] >> (8 * (i % 4))));
-                                mA = fmaxf(mA, yA[i] + f);
-                                mB = fmaxf(mB, yB[i] + f);
-                            }
-                            mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 16));
-                            mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 16));
-                            top = lane < 16 ? mA : mB;
-                        }
+                    if (!__all_sync(0xffffffffu, Ref::stays(top, R))) {
                         const float was = R;
-                        R = Ref::moved(top, R, R == last, n, *ask, low, peak);
+                        R = Ref::moved(top, R, R == last, n, ask->eager != 0, low, peak);
                         d = ref_exp(was, R);
                         RA = __shfl_sync(0xffffffffu, R, lane & 15);
                         RB = __shfl_sync(0xffffffffu, R, 16 + (lane & 15));
@@ -565,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     float2 sA = make_float2(0.f, 0.f), sB = sA, rA = sA, rB = sA;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        // 1 / s, as bf16 (2^kZeroDown / s for tokens whose latents are all zero)
+                        // 1 / s, as bf16 (of lifted tokens, 2^m / s)
                         const uint4 sw = sw4[k + kScaleInv / 16];
                         const uint32_t sb4[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll
@@ -619,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     *reinterpret_cast<uint4*>(al) = make_uint4(loA[0], loA[1], loA[2], loA[3]);
                     *reinterpret_cast<uint4*>(al + 2048) = make_uint4(loB[0], loB[1], loB[2], loB[3]);
                     reinterpret_cast<int8_t*>(stage + kPBytes)[(cq & 1) * kRows + r] = static_cast<int8_t>(d);
+                    if ((warp & 7) == 0 && lane == 0) *reinterpret_cast<uint32_t*>(stage + kPBytes + 2 * kRows) = ask->lift;
                     fence_proxy_async_cta();
                     mbar_arrive(&bars[kSBarStaged + stg]);
                     stg += 2;
@@ -699,10 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                          mbar_wait(&bars[kSBarFull + 2 * sb + 1], us & 1u, abort_flag, kLimitNs);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    // (the buffer of f is free already: SEmpty of the tile before this one has been seen)
+                    // (the buffer of lifts is free already: SEmpty of the tile before this one has been seen)
                     uint8_t* buf = smem + kSOffScale + (n % kScaleBufs) * kScaleBytes;
                     const TileAsks ask = scan.tile(smem + kSOffRing + sb * kTileBytes, min(kTile, s.L - t * kTile), bits, lane,
-                                                     Ref::kHalf, reinterpret_cast<int8_t*>(buf + kScaleF));
+                                                    buf + kScaleF);
                     if (lane < 2) mbar_arrive(&bars[kSBarEmpty + 2 * sb + lane]);
                     ok = mbar_wait(&bars[kSBarSEmpty + sb], (us & 1u) ^ 1u, abort_flag, kLimitNs);
                     uint32_t e[4];
@@ -711,16 +698,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                     uint8_t* to = buf + 8 * lane;
                     const uint2 sc = make_uint2(__byte_perm(bits[0], bits[1], 0x7632), __byte_perm(bits[2], bits[3], 0x7632));
                     uint2 is = make_uint2(0x7F007F00u - sc.x, 0x7F007F00u - sc.y);
-                    if (ask.with_f) {
+                    if (ask.lift) {
                         const uint32_t f = *reinterpret_cast<const uint32_t*>(buf + kScaleF + 4 * lane);
                         uint32_t up[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            up[i] = 0;
-                            if (static_cast<int8_t>(f >> (8 * i)) == static_cast<int>(kZeroF)) {
-                                e[i] = __float_as_uint(__uint_as_float(e[i]) - kZeroDown);
-                                up[i] = static_cast<uint32_t>(kZeroDown) << 7;
-                            }
+                            const uint32_t m = f >> (8 * i) & 0xFFu;
+                            e[i] = __float_as_uint(__uint_as_float(e[i]) - static_cast<float>(m));
+                            up[i] = m << 7;
                         }
                         is.x += up[0] | (up[1] << 16);
                         is.y += up[2] | (up[3] << 16);
@@ -829,6 +814,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         }
                         ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
+                        // lifted tokens' codes (as the S CTA's scan has found them in the same codes)
+                        if (h == 0 && *reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes + 2 * kRows) != 0) {
+                            ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            uint8_t* v = smem + kOOffV + st * kVBytes;
+                            const uint2 l = tile_lifts(v, nvalid, small_tokens(v, nvalid, lane), lane);
+                            __syncwarp();
+                            for (int i = 0; i < 4; ++i)
+                                if (32 * i + lane < nvalid) lift_row(v + (32 * i + lane) * 128, static_cast<int>(l.x >> (8 * i) & 0xFFu));
+                            fence_proxy_async_cta();
+                            __syncwarp();
+                        }
                         // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN); rows that not every query sees:
                         // NaN made 0
                         const int some = max(0, s.L - p.n_q + 1 - t * kTile);

@@ -265,3 +265,13 @@ def test_decode8_ragged_peaks_zeros_and_scales_together(H, n_q, splits):
     for _ in range(10):
         o2, l2 = p.decode(num_splits=splits)
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("H", [16, 24, 40, 128])
+@pytest.mark.parametrize("ratio", [1.0, 4.0, 20.0, 64.0, 1000.0])
+def test_decode8_tail_behind_a_peak_in_a_short_sequence(H, ratio):
+    """One or a few tiles: the peak's own unit holds a good part of the tail."""
+    for n in (33, 64, 100, 128, 200, 300):
+        for at in (0, n // 2, n - 1):
+            for mass in (0.05, 0.5):
+                check(peaked(n, H, mass=mass, at=at, ratio=ratio, mean=0.3), num_splits=1)
