@@ -814,19 +814,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                         }
                         ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
-                        // lifted tokens' codes (as the S CTA's scan has found them in the same codes)
-                        if (h == 0 && *reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes + 2 * kRows) != 0) {
-                            ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            uint8_t* v = smem + kOOffV + st * kVBytes;
-                            const uint2 l = tile_lifts(v, nvalid, small_tokens(v, nvalid, lane), lane);
-                            __syncwarp();
-                            for (int i = 0; i < 4; ++i)
-                                if (32 * i + lane < nvalid) lift_row(v + (32 * i + lane) * 128, static_cast<int>(l.x >> (8 * i) & 0xFFu));
-                            fence_proxy_async_cta();
-                            __syncwarp();
-                        }
+                        // (read by every lane: which of the two units move some row's reference, whether tokens are lifted: the
+                        // S CTA's scan has found them in the same codes)
+                        const uint32_t* moved = reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes);
+                        const uint32_t moved0 = moved[lane], moved1 = moved[32 + lane], lift = moved[64];
+                        const bool resc0 = __any_sync(0xffffffffu, moved0 != 0);
+                        const bool resc1 = __any_sync(0xffffffffu, moved1 != 0);
+                        if (h == 0 && lift != 0)
+                            lift_tile(smem + kOOffV + st * kVBytes, nvalid, lane, smem_u32(&bars[kOBarVFull + st]),
+                                      (n / kVStages) & 1u);
                         // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN); rows that not every query sees:
                         // NaN made 0
                         const int some = max(0, s.L - p.n_q + 1 - t * kTile);
@@ -845,10 +841,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                         }
-                        // (read by every lane: which of the two units move some row's reference)
-                        const uint32_t* moved = reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes);
-                        const bool resc0 = __any_sync(0xffffffffu, moved[lane] != 0);
-                        const bool resc1 = __any_sync(0xffffffffu, moved[32 + lane] != 0);
 #pragma unroll 1
                         for (int kk = 0; kk < 2; ++kk) {
                             const bool fresh = (t == s.t0 && h == 0 && kk == 0);
