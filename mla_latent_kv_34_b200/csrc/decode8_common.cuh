@@ -386,17 +386,15 @@ static __device__ __noinline__ uint2 tile_lifts(const uint8_t* codes, int n, uin
     return make_uint2(use ? lifts : 0u, (use ? 1u : 0u) | (g <= -kFar ? 2u : 0u));
 }
 
-// A tile's lifts, applied to a copy of its codes (by a warp, one lane of which has seen the barrier of the copy's phase
-// `parity`: each lane looks at it once more, which orders its own reads after the copy).
-static __device__ __noinline__ void lift_tile(uint8_t* codes, int n, int lane, uint32_t bar, uint32_t parity) {
-    mbar_poll(bar, parity);
-    const uint2 l = tile_lifts(codes, n, small_tokens(codes, n, lane), lane);
+// A tile's lifts, applied to a copy of its codes by a warp; whether there are any.
+static __device__ __noinline__ bool lift_tile(uint8_t* codes, int n, uint32_t small, int lane) {
+    const uint2 l = tile_lifts(codes, n, small, lane);
     __syncwarp();
 #pragma unroll 1
     for (int i = 0; i < 4; ++i)
         if (32 * i + lane < n) lift_row(codes + (32 * i + lane) * 128, static_cast<int>(l.x >> (8 * i) & 0xFFu));
-    fence_proxy_async_cta();
     __syncwarp();
+    return (l.y & 1u) != 0;
 }
 
 // One warp scans the tiles of a segment one after another, from the codes that the copies brought to shared memory.  (The

@@ -25,7 +25,7 @@
 // instruction cache: code that is seldom run is kept short or called.  At B 32, H 128, 8K the attend phase takes 97 to 101 us
 // (45 at the bf16 rate), of which 12 are the
 // start (queries to codes, first tile) and as many a second sequence's start; 4 x 128K 161 (89), ragged 128 x 2 tokens of
-// 1 to 32K 1.29 ms a call (736 us).  A move of some row's reference costs the tile a pass over O, 1 us:
+// 1 to 32K 1.29 ms a call (736 us; before the O CTA's look at V had a warp of its own).  A move of some row's reference costs the tile a pass over O, 1 us:
 // scores with a standard deviation of 3 at B 32, H 128, 8K take 207 us a call instead of 115.  A first form on CUDA cores took
 // 7.3, 14.6 and 89 ms; without the scan of the tiles (TileAsks) and with a reference that only rises it took 1.95 to 2.05 us a
 // tile, 1.18 ms a ragged call, and lost tails.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 -> 93.9 us),
@@ -90,7 +90,8 @@ constexpr int kOOffMsg = kVStages * kVBytes;
 constexpr int kOOffBar = kOOffMsg + kPSlots * kMsgStride;
 constexpr int kOBarVFull = 0, kOBarVEmpty = kVStages, kOBarPFull = 2 * kVStages, kOBarOFull = kOBarPFull + kPSlots,
               kOBarOFree = kOBarOFull + 1, kOBarRescReq = kOBarOFree + 1, kOBarRescDone = kOBarRescReq + 1,
-              kOBarODrain = kOBarRescDone + 1, kOBarFin = kOBarODrain + 1, kONumBars = kOBarFin + 1;
+              kOBarODrain = kOBarRescDone + 1, kOBarFin = kOBarODrain + 1, kOBarReady = kOBarFin + 1,
+              kONumBars = kOBarReady + kVStages;
 constexpr int kOOffTail = kOOffBar + kONumBars * 8;
 constexpr int kTailBytes = 32;  // tmem base, abort flag, resc slot, [tile total, first sequence, its first tile]
 constexpr int kSmemBytes = (kSOffTail > kOOffTail ? kSOffTail : kOOffTail) + kTailBytes;
@@ -170,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
         } else {
             for (int i = 0; i < kVStages; ++i) {
                 mbar_init(&bars[kOBarVFull + i], 1);
-                mbar_init(&bars[kOBarVEmpty + i], 1);
+                mbar_init(&bars[kOBarVEmpty + i], 2);  // the aggregation's MMAs and the look at its rows
+                mbar_init(&bars[kOBarReady + i], 1);
             }
             // a message slot's barrier is armed here, not by the sender: a remote arrive (a release at cluster scope)
             // held the sender up for about 2000 cycles a message
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
             const bool leader = elect_one();
             SegWalk w = walk;
             Seg s;
-            uint32_t n = 0, kseg = 0, nresc = 0;
+            uint32_t n = 0, kseg = 0, nresc = 0, nready = 0;  // (nready: bit st, the phase of kOBarReady + st)
             bool ok = true;
             while (ok && w.next(p, s)) {
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
@@ -810,36 +812,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                             if (ok) mbar_arrive_expect_tx(&bars[kOBarPFull + pb], kMsgBytes);  // for its next message
                             if (ok && t == s.t0 && h == 0)
                                 ok = mbar_wait(&bars[kOBarOFree], (kseg & 1u) ^ 1u, abort_flag, kLimitNs);
-                            if (ok && h == 0) ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
+                            if (ok && h == 0) {
+                                ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
+                                // tokens are lifted (the S CTA's scan has found them in the same codes), or not seen by every query
+                                if (*reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes + 2 * kRows) != 0 ||
+                                    s.L - p.n_q + 1 - t * kTile < nvalid) {
+                                    ok = ok && mbar_wait(&bars[kOBarReady + st], nready >> st & 1u, abort_flag, kLimitNs);
+                                    nready ^= 1u << st;
+                                }
+                            }
                         }
                         ok = __any_sync(0xffffffffu, ok && leader);
                         if (!ok) break;
-                        // (read by every lane: which of the two units move some row's reference, whether tokens are lifted: the
-                        // S CTA's scan has found them in the same codes)
+                        // (read by every lane: which of the two units move some row's reference)
                         const uint32_t* moved = reinterpret_cast<const uint32_t*>(smem + kOOffMsg + pb * kMsgStride + kPBytes);
-                        const uint32_t moved0 = moved[lane], moved1 = moved[32 + lane], lift = moved[64];
+                        const uint32_t moved0 = moved[lane], moved1 = moved[32 + lane];
                         const bool resc0 = __any_sync(0xffffffffu, moved0 != 0);
                         const bool resc1 = __any_sync(0xffffffffu, moved1 != 0);
-                        if (h == 0 && lift != 0)
-                            lift_tile(smem + kOOffV + st * kVBytes, nvalid, lane, smem_u32(&bars[kOBarVFull + st]),
-                                      (n / kVStages) & 1u);
-                        // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN); rows that not every query sees:
-                        // NaN made 0
-                        const int some = max(0, s.L - p.n_q + 1 - t * kTile);
-                        if (h == 0 && some < kTile) {
-                            uint8_t* v = smem + kOOffV + st * kVBytes;
-                            if (some < nvalid) {
-                                ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
-                                nan_to_zero_rows(v, some, nvalid, lane);
-                            }
+                        if (h == 0 && nvalid < kTile) {
+                            // rows past the sequence end: P is 0 there, make V 0 too (no 0 * NaN)
                             const int nz = (kTile - nvalid) * 8;  // 16-byte units per chunk
                             for (int i = lane; i < 4 * nz; i += 32) {
                                 const int c = i / nz, q = i % nz;
-                                *reinterpret_cast<uint4*>(v + c * kChunk + nvalid * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(smem + kOOffV + st * kVBytes + c * kChunk + nvalid * 128 + q * 16) =
+                                    make_uint4(0, 0, 0, 0);
                             }
                             fence_proxy_async_cta();
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
                         }
 #pragma unroll 1
                         for (int kk = 0; kk < 2; ++kk) {
@@ -888,6 +886,38 @@ __global__ void __launch_bounds__(kThreads, 1) decode8_tc_kernel(const Params p)
                 mbar_wait(&bars[kOBarFin], 0, &never, kLimitNs);
             }
             __syncwarp();
+        } else if (warp == kWarpScale) {
+            // ---- what V's rows need before they are multiplied: small tokens lifted, NaN in rows that not every query sees made
+            //      0 (P = 0 times NaN).  The MMA warp waits for it where there is such a row; a stage stays until it has been
+            //      looked at.
+            SegWalk w = walk;
+            Seg s;
+            uint32_t n = 0;
+            bool ok = true;
+            while (ok && w.next(p, s)) {
+                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                    const uint32_t st = n % kVStages;
+                    ok = mbar_wait(&bars[kOBarVFull + st], (n / kVStages) & 1u, abort_flag, kLimitNs);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t* v = smem + kOOffV + st * kVBytes;
+                    const int nvalid = min(kTile, s.L - t * kTile), some = max(0, s.L - p.n_q + 1 - t * kTile);
+                    const uint32_t small = small_tokens(v, nvalid, lane);
+                    bool touched = false;
+                    if (__any_sync(0xffffffffu, small != 0)) touched = lift_tile(v, nvalid, small, lane);
+                    if (some < nvalid) {
+                        nan_to_zero_rows(v, some, nvalid, lane);
+                        touched = true;
+                    }
+                    if (touched) fence_proxy_async_cta();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (touched) mbar_arrive(&bars[kOBarReady + st]);
+                        mbar_arrive(&bars[kOBarVEmpty + st]);
+                    }
+                }
+            }
+            if (!ok && lane == 0) raise_abort(abort_flag, peer_abort, p.dev_status);
         } else if (warp < kSoftWarps) {
             // ---- epilogue: warp (qd, cq), one thread per query row and 128 columns
             const int r = 32 * (warp & 3) + lane, cq = warp >> 2;
