@@ -25,8 +25,8 @@
 // instruction cache: code that is seldom run is kept short or called.  At B 32, H 128, 8K the attend phase takes 97 to 101 us
 // (45 at the bf16 rate), of which 12 are the
 // start (queries to codes, first tile) and as many a second sequence's start; 4 x 128K 161 (89), ragged 128 x 2 tokens of
-// 1 to 32K 1.29 ms a call (736 us; before the O CTA's look at V had a warp of its own).  A move of some row's reference costs the tile a pass over O, 1 us:
-// scores with a standard deviation of 3 at B 32, H 128, 8K take 207 us a call instead of 115.  A first form on CUDA cores took
+// 1 to 32K 1.2 ms a call, 1.25 to 1.31 one after another (736 us).  A move of some row's reference costs the tile a pass over O, 1 us:
+// scores with a standard deviation of 3 at B 32, H 128, 8K take 210 us a call instead of 112.  A first form on CUDA cores took
 // 7.3, 14.6 and 89 ms; without the scan of the tiles (TileAsks) and with a reference that only rises it took 1.95 to 2.05 us a
 // tile, 1.18 ms a ragged call, and lost tails.  Looked at and left: bringing later tiles to L2 ahead of the ring (slower: 90.9 -> 93.9 us),
 // all of a query's loads before the first is used (more registers and code: 91 -> 96 us), scanning from global memory (its
